@@ -2,7 +2,9 @@
  * nvfp4.h — C ABI of libnvfp4.so: the NVFP4 linear layer of a VLA action head on B200
  * (sm_100a): bf16 -> {LayerNorm | RMSNorm | AdaLN | AdaRMSNorm} -> dynamic NVFP4 quantize,
  * offline NVFP4 weight quantize, and a block-scaled NVFP4 GEMM (tcgen05 kind::mxf4nvf4)
- * with fused bias / residual / tanh-GELU->FP4 / GeGLU->FP4 epilogues.
+ * with fused bias / residual / tanh-GELU->FP4 / GeGLU->FP4 epilogues; and, between the QKV
+ * and the attention-output GEMM, per-head norm + rotation, an NVFP4 key/value cache and
+ * attention.
  *
  * Sources are cited as "page title, section":
  *   [GROOT]  "GROOT N1.7 update: Thor NVFP4 + FA4 performance tier"
@@ -153,7 +155,9 @@ nvfp4_status nvfp4_sf_zero(uint8_t *sf, int rows, int K, nvfp4_stream_t stream);
 size_t nvfp4_gemm_workspace_bytes(int M, int N, int K);
 
 /* Reads and clears the library's device status word after synchronising `stream`:
- * NVFP4_OK, or NVFP4_ERR_TIMEOUT if a kernel's bounded wait expired since the last read. */
+ * NVFP4_OK, NVFP4_ERR_TIMEOUT if a kernel's bounded wait expired since the last read, or
+ * NVFP4_ERR_INVALID_ARG if nvfp4_qk_norm_rope or nvfp4_kv_read met a position or row that
+ * does not exist (the first of the two is kept). */
 nvfp4_status nvfp4_get_device_status(nvfp4_stream_t stream);
 
 /* Diagnostics (tracing): while `buf` (device, `words` 64-bit words) is set, each
@@ -418,6 +422,95 @@ nvfp4_status nvfp4_program_build(const nvfp4_op *ops, int n_ops, void *buffer, s
 /* Runs the grouped GEMM on `stream`: one launch.  Allocates nothing; capturable in a CUDA
  * graph.  Runs of the same program must not overlap. */
 nvfp4_status nvfp4_program_run(const nvfp4_program *prog, nvfp4_stream_t stream);
+
+/* ---- attention side of a layer: heads, key/value cache, attention --------------------- */
+
+/* A bf16 [B, T, H, D] view in device memory: strides in elements, the D elements of a head
+ * adjacent.  The pointer must be 16-byte aligned and the strides of dimensions longer than 1
+ * multiples of 8, >= 0 (an input's stride may be 0: a broadcast dimension; an output's rows
+ * must not overlap). */
+typedef struct {
+    void *ptr;
+    int64_t stride_b, stride_t, stride_h;
+} nvfp4_heads;
+
+/* A key/value cache in NVFP4: per sequence and key head, `capacity` rows of D elements.
+ *   codes : uint8 [B, H, capacity, D/2], element 2j in the low nibble of byte j (E2M1)
+ *   sf    : uint8 [B, H, capacity, D/16], the UE4M3 scale of each 16-element block, row-major
+ *           (rows are read and written one by one, so not in the GEMM operands' atoms)
+ *   k_scale, v_scale: the fp32 global scales; an element is val(code) * dec(sf) * scale.
+ * Rows [0, length) may be written and read; length <= capacity.  capacity % 16 == 0,
+ * D % 16 == 0, 16 <= D <= 256, dense, every pointer 16-byte aligned. */
+typedef struct {
+    uint8_t *k_codes, *k_sf, *v_codes, *v_sf;
+    float k_scale, v_scale;
+    int B, H, capacity, D, length;
+} nvfp4_kv_cache;
+
+/* Per-head norm and position rotation of queries and keys, in one pass over them; with a cache,
+ * the keys and the values are quantized into it in the same launch. */
+typedef struct {
+    int B, T;     /* tokens */
+    int Hq, Hkv;  /* heads of q (0: none) and of k and v (0: none) */
+    int D;        /* head size: D % 16 == 0, 16 <= D <= 256 */
+    int R;        /* rotated elements of a head, the first R: R % 16 == 0, 0 <= R <= D (0: none) */
+    int pairs;    /* 0: elements i and i + R/2 are a pair, 1: elements 2i and 2i + 1 */
+    int norm;     /* 1: n = (x * rstd) * gamma, rstd = 1/sqrt(mean(x^2) + eps); 0: n = x */
+    float eps;
+    nvfp4_heads q, k, v;            /* v: with a cache only */
+    nvfp4_heads q_out, k_out;       /* k_out: without a cache only; may be q / k themselves */
+    const void *q_gamma, *k_gamma;  /* bf16 [D] or NULL (1) */
+    const float *table;             /* fp32 [table_rows, R]: cos, then sin, of the R/2 angles (R > 0) */
+    int table_rows;
+    const int32_t *positions;       /* [B, T] table rows; NULL: start[b] + t */
+    const int32_t *start;           /* [B] cache row of each sequence's token 0; NULL: 0 */
+    const int32_t *count;           /* [B] tokens of each sequence in this call; NULL: T */
+    const nvfp4_kv_cache *cache;    /* host pointer; NULL: k goes to k_out */
+} nvfp4_qk_args;
+
+/* For each token t < count[b] and head:
+ *   rstd in fp64 sums, rounded once to fp32; n = (x * rstd) * gamma;
+ *   a pair (a, b) at angle index i: (a cos_i - b sin_i, b cos_i + a sin_i), each operation one
+ *   fp32 rounding; elements from R on pass;
+ * stored as bf16 to q_out / k_out, or, for k with a cache, quantized from fp32 as
+ * nvfp4_quantize_norm quantizes (per 16 elements, global scale k_scale) into cache row
+ * start[b] + t; v's rows go there unnormalized and unrotated.  With Hq = 0, norm = 0 and R = 0
+ * it is the plain cache write.  Tokens from count[b] on are left alone.  A token whose table
+ * row or cache row does not exist is left alone too, and nvfp4_get_device_status reports
+ * NVFP4_ERR_INVALID_ARG.  Each output may be its own input, and otherwise overlaps no input. */
+nvfp4_status nvfp4_qk_norm_rope(const nvfp4_qk_args *a, nvfp4_stream_t stream);
+
+/* Reads `length` rows of each sequence from row start[b] (device, [B]; NULL: 0) on back to
+ * bf16: k_out, v_out [B, length, H, D], each element val(code) * dec(sf) (exact) * scale,
+ * rounded once.  Rows outside [0, cache->length) are written as zeros, and reported as above.
+ * Either output's ptr may be NULL. */
+nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache *cache, const int32_t *start, int length, nvfp4_heads k_out,
+                           nvfp4_heads v_out, nvfp4_stream_t stream);
+
+typedef struct {
+    int B, T;       /* sequences, queries of each */
+    int S;          /* key rows: of k and v, or <= cache->length */
+    int Hq, Hkv;    /* Hq % Hkv == 0: query head h reads key head h / (Hq / Hkv) */
+    int D;          /* head size: D % 8 == 0, 8 <= D <= 256 (a cache: D % 16 == 0) */
+    float scale;    /* > 0, finite */
+    nvfp4_heads q, k, v, out;    /* k, v [B, S, Hkv, D] bf16: without a cache only */
+    const int32_t *kv_len;       /* [B] keys of each sequence, clamped to [0, S]; NULL: S */
+    const uint8_t *key_mask;     /* [B, S], 0: the key is left out; NULL: none is */
+    int64_t mask_stride;         /* elements between the mask's sequences */
+    const nvfp4_kv_cache *cache; /* host pointer; NULL: k and v */
+    void *workspace;
+    size_t ws_bytes;
+} nvfp4_attention_args;
+
+/* out[b, t, h] = sum_j p_j v_j,  p = softmax_j(scale * q[b, t, h] . k_j) over the keys
+ * j < kv_len[b] with key_mask[b, j] != 0; zero where there is no such key.  What the keys and
+ * values of left-out places hold (infinities and NaN too) has no influence.  Scores,
+ * statistics and sums are fp32; the softmax weights are rounded to bf16 (bf16 keys and
+ * values) or fp16 (cache) for their product with the values; out is rounded once to bf16.
+ * B, T, S = 0: nothing is read (S = 0: zeros are written).  Results do not depend on timing.
+ * workspace: nvfp4_attention_workspace_bytes, used by one call at a time, any contents. */
+nvfp4_status nvfp4_attention(const nvfp4_attention_args *a, nvfp4_stream_t stream);
+size_t nvfp4_attention_workspace_bytes(const nvfp4_attention_args *a);
 
 #ifdef __cplusplus
 }

@@ -14,8 +14,10 @@
 #include <vector>
 
 #include "../../include/nvfp4.h"
+#include "attention.h"
 #include "gemm.h"
 #include "norm.h"
+#include "sm100.cuh"
 
 namespace nvfp4 {
 // mma_rate.cu: one CTA issues `ksteps` K steps of block-scaled MMAs (mode 0) or of scale
@@ -443,6 +445,76 @@ nvfp4_status norm_impl(const void *x, nvfp4_in_dtype dt, int M, int K, int ldx, 
     return from_cuda(e);
 }
 
+// ---- attention side --------------------------------------------------------------------------
+
+// A bf16 [B, T, H, D] view: pointer, alignment and strides.  Strides of dimensions that are not
+// longer than 1 are not used: they become 0.
+nvfp4_status check_heads(const nvfp4_heads &v, int B, int T, int H, int D, bool output, Heads *out) {
+    if (v.ptr == nullptr) return NVFP4_ERR_INVALID_ARG;
+    const long long sb = B > 1 ? v.stride_b : 0, st = T > 1 ? v.stride_t : 0, sh = H > 1 ? v.stride_h : 0;
+    constexpr long long kMaxStride = 1ll << 38;  // a tensor map's strides end at 2^40 bytes
+    for (long long s : {sb, st, sh})
+        if (s < 0 || s > kMaxStride) return NVFP4_ERR_INVALID_ARG;
+    if (!aligned16(v.ptr) || sb % 8 != 0 || st % 8 != 0 || sh % 8 != 0) return NVFP4_ERR_MISALIGNED;
+    if (output && ((B > 1 && sb < D) || (T > 1 && st < D) || (H > 1 && sh < D))) return NVFP4_ERR_INVALID_ARG;
+    *out = Heads{static_cast<uint16_t *>(v.ptr), sb, st, sh};
+    return NVFP4_OK;
+}
+
+nvfp4_status check_cache(const nvfp4_kv_cache &c, int B, int H, int D, Cache *out) {
+    if (c.capacity < 0 || ((c.k_codes == nullptr || c.k_sf == nullptr || c.v_codes == nullptr || c.v_sf == nullptr) &&
+                           B > 0 && c.capacity > 0))
+        return NVFP4_ERR_INVALID_ARG;
+    if (c.B != B || c.H != H || c.D != D || c.length < 0 || c.length > c.capacity) return NVFP4_ERR_INVALID_ARG;
+    if (c.capacity % 16 != 0 || D % 16 != 0 || D > 256) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (!scale_ok(c.k_scale) || !scale_ok(c.v_scale)) return NVFP4_ERR_INVALID_ARG;
+    if (!aligned16(c.k_codes) || !aligned16(c.k_sf) || !aligned16(c.v_codes) || !aligned16(c.v_sf))
+        return NVFP4_ERR_MISALIGNED;
+    *out = Cache{{c.k_codes, c.k_sf, c.k_scale}, {c.v_codes, c.v_sf, c.v_scale}, c.H, c.capacity, c.length};
+    return NVFP4_OK;
+}
+
+// The arguments of nvfp4_attention, without device access; `empty`: there is nothing to write.
+nvfp4_status attention_args(const nvfp4_attention_args &x, AttnArgs *a, bool *empty) {
+    if (x.B < 0 || x.T < 0 || x.S < 0 || x.Hq <= 0 || x.Hkv <= 0 || x.D <= 0) return NVFP4_ERR_INVALID_ARG;
+    if (x.Hq % x.Hkv != 0 || x.D % 8 != 0 || x.D > 256) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (!(x.scale > 0.0f) || !std::isfinite(x.scale)) return NVFP4_ERR_INVALID_ARG;
+    // row and key counts stay within 32 bits
+    if (static_cast<long long>(x.T) * x.Hq > 0x3FFFFFFFLL || x.S > 0x3FFFFFFF) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    *a = AttnArgs{};
+    *empty = x.B == 0 || x.T == 0;
+    nvfp4_status st = NVFP4_OK;
+    if (x.cache != nullptr) {
+        st = check_cache(*x.cache, x.B, x.Hkv, x.D, &a->cache);
+        if (st == NVFP4_OK && x.S > x.cache->length) st = NVFP4_ERR_INVALID_ARG;
+    }
+    if (st != NVFP4_OK || *empty) return st;
+    st = check_heads(x.q, x.B, x.T, x.Hq, x.D, false, &a->q);
+    if (st == NVFP4_OK) st = check_heads(x.out, x.B, x.T, x.Hq, x.D, true, &a->out);
+    if (st == NVFP4_OK && x.cache == nullptr && x.S > 0) {
+        st = check_heads(x.k, x.B, x.S, x.Hkv, x.D, false, &a->k);
+        if (st == NVFP4_OK) st = check_heads(x.v, x.B, x.S, x.Hkv, x.D, false, &a->v);
+    }
+    if (st != NVFP4_OK) return st;
+    if (x.key_mask != nullptr && (x.mask_stride < 0 || (x.B > 1 && x.mask_stride != 0 && x.mask_stride < x.S)))
+        return NVFP4_ERR_INVALID_ARG;
+    if (x.kv_len != nullptr && (reinterpret_cast<uintptr_t>(x.kv_len) & 3u) != 0) return NVFP4_ERR_MISALIGNED;
+    a->B = x.B;
+    a->T = x.T;
+    a->S = x.S;
+    a->Hq = x.Hq;
+    a->Hkv = x.Hkv;
+    a->D = x.D;
+    a->G = x.Hq / x.Hkv;
+    a->cached = x.cache != nullptr ? 1 : 0;
+    a->scale_log2 = static_cast<float>(static_cast<double>(x.scale) * 1.4426950408889634 *
+                                       (a->cached ? static_cast<double>(a->cache.k.g) : 1.0));
+    a->kv_len = x.kv_len;
+    a->mask = x.key_mask;
+    a->mask_stride = x.B > 1 ? x.mask_stride : 0;
+    return NVFP4_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -453,7 +525,7 @@ nvfp4_status nvfp4_probe(void) {
     // the kernels of this library must load on the device
     if (probe_norm_kernels() != cudaSuccess || probe_gemm_kernels() != cudaSuccess ||
         probe_gemm_persistent() != cudaSuccess ||
-        probe_gemm_grouped() != cudaSuccess) {
+        probe_gemm_grouped() != cudaSuccess || probe_attention() != cudaSuccess) {
         cudaGetLastError();
         return NVFP4_ERR_UNSUPPORTED_DEVICE;
     }
@@ -549,7 +621,7 @@ nvfp4_status nvfp4_mma_rate(int n, int mode, int ksteps, double *issue_cycles, d
 nvfp4_status nvfp4_get_device_status(nvfp4_stream_t stream) {
     uint32_t v = 0;
     if (read_and_clear_device_status(stream, &v) != cudaSuccess) return NVFP4_ERR_CUDA;
-    return v == 0 ? NVFP4_OK : NVFP4_ERR_TIMEOUT;
+    return v == kStatusOk ? NVFP4_OK : v == kStatusBadIndex ? NVFP4_ERR_INVALID_ARG : NVFP4_ERR_TIMEOUT;
 }
 
 nvfp4_status nvfp4_quantize_norm(const void *x, nvfp4_in_dtype dt, int M, int K, int ldx, nvfp4_norm kind,
@@ -858,6 +930,111 @@ nvfp4_status nvfp4_program_run(const nvfp4_program *prog, nvfp4_stream_t stream)
         return from_cuda(e);
     }
     return NVFP4_ERR_INVALID_ARG;  // not a program this library built
+}
+
+// ---- attention side --------------------------------------------------------------------------
+nvfp4_status nvfp4_qk_norm_rope(const nvfp4_qk_args *x, nvfp4_stream_t stream) {
+    if (x == nullptr) return NVFP4_ERR_INVALID_ARG;
+    if (x->B < 0 || x->T < 0 || x->Hq < 0 || x->Hkv < 0 || x->D <= 0) return NVFP4_ERR_INVALID_ARG;
+    if ((x->pairs != 0 && x->pairs != 1) || (x->norm != 0 && x->norm != 1)) return NVFP4_ERR_INVALID_ARG;
+    if (x->R < 0 || x->R > x->D) return NVFP4_ERR_INVALID_ARG;
+    if (x->D % 16 != 0 || x->D > 256 || x->R % 16 != 0) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (x->norm && (!(x->eps >= 0.0f) || !std::isfinite(x->eps))) return NVFP4_ERR_INVALID_ARG;
+    if (!x->norm && (x->q_gamma != nullptr || x->k_gamma != nullptr)) return NVFP4_ERR_INVALID_ARG;
+    QkArgs a = {};
+    const bool cached = x->cache != nullptr;
+    nvfp4_status st = NVFP4_OK;
+    if (cached) {
+        if (x->Hkv == 0) return NVFP4_ERR_INVALID_ARG;
+        st = check_cache(*x->cache, x->B, x->Hkv, x->D, &a.cache);
+        if (st != NVFP4_OK) return st;
+    }
+    if (x->B == 0 || x->T == 0 || (x->Hq == 0 && x->Hkv == 0)) return NVFP4_OK;
+    if (x->R > 0 && (x->table == nullptr || x->table_rows <= 0)) return NVFP4_ERR_INVALID_ARG;
+    if (x->Hq > 0) {
+        st = check_heads(x->q, x->B, x->T, x->Hq, x->D, false, &a.q);
+        if (st == NVFP4_OK) st = check_heads(x->q_out, x->B, x->T, x->Hq, x->D, true, &a.q_out);
+    }
+    if (st == NVFP4_OK && x->Hkv > 0) {
+        st = check_heads(x->k, x->B, x->T, x->Hkv, x->D, false, &a.k);
+        if (st == NVFP4_OK)
+            st = cached ? check_heads(x->v, x->B, x->T, x->Hkv, x->D, false, &a.v)
+                        : check_heads(x->k_out, x->B, x->T, x->Hkv, x->D, true, &a.k_out);
+    }
+    if (st != NVFP4_OK) return st;
+    for (const void *p : {x->q_gamma, x->k_gamma, static_cast<const void *>(x->R > 0 ? x->table : nullptr)})
+        if (p != nullptr && !aligned16(p)) return NVFP4_ERR_MISALIGNED;
+    for (const int32_t *p : {x->positions, x->start, x->count})
+        if ((reinterpret_cast<uintptr_t>(p) & 3u) != 0) return NVFP4_ERR_MISALIGNED;
+    // one group of lanes per head and token: their number stays within a grid
+    if (static_cast<double>(x->B) * x->T * (x->Hq + 2.0 * x->Hkv) > 1.6e10) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    st = check_device();
+    if (st != NVFP4_OK) return st;
+    a.B = x->B;
+    a.T = x->T;
+    a.Hq = x->Hq;
+    a.Hkv = x->Hkv;
+    a.D = x->D;
+    a.R = x->R;
+    a.inter = x->pairs;
+    a.norm = x->norm;
+    a.eps = x->eps;
+    a.q_gamma = static_cast<const uint16_t *>(x->q_gamma);
+    a.k_gamma = static_cast<const uint16_t *>(x->k_gamma);
+    a.table = x->table;
+    a.table_rows = x->table_rows;
+    a.positions = x->positions;
+    a.start = x->start;
+    a.count = x->count;
+    a.cached = cached ? 1 : 0;
+    if ((a.status = status_word()) == nullptr) return NVFP4_ERR_CUDA;
+    cudaError_t e = launch_qk_norm_rope(a, stream);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    return from_cuda(e);
+}
+
+nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache *cache, const int32_t *start, int length, nvfp4_heads k_out,
+                           nvfp4_heads v_out, nvfp4_stream_t stream) {
+    if (cache == nullptr || length < 0 || cache->B < 0 || cache->H <= 0 || cache->D <= 0) return NVFP4_ERR_INVALID_ARG;
+    ReadArgs a = {};
+    nvfp4_status st = check_cache(*cache, cache->B, cache->H, cache->D, &a.cache);
+    if (st != NVFP4_OK) return st;
+    if (cache->B == 0 || length == 0 || (k_out.ptr == nullptr && v_out.ptr == nullptr)) return NVFP4_OK;
+    if (k_out.ptr != nullptr) st = check_heads(k_out, cache->B, length, cache->H, cache->D, true, &a.k_out);
+    if (st == NVFP4_OK && v_out.ptr != nullptr)
+        st = check_heads(v_out, cache->B, length, cache->H, cache->D, true, &a.v_out);
+    if (st != NVFP4_OK) return st;
+    if ((reinterpret_cast<uintptr_t>(start) & 3u) != 0) return NVFP4_ERR_MISALIGNED;
+    if (static_cast<double>(cache->B) * length * cache->H > 1.6e10) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    st = check_device();
+    if (st != NVFP4_OK) return st;
+    a.B = cache->B;
+    a.L = length;
+    a.H = cache->H;
+    a.D = cache->D;
+    a.start = start;
+    if ((a.status = status_word()) == nullptr) return NVFP4_ERR_CUDA;
+    cudaError_t e = launch_kv_read(a, stream);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    return from_cuda(e);
+}
+
+size_t nvfp4_attention_workspace_bytes(const nvfp4_attention_args *x) {
+    (void)x;
+    return 0;
+}
+
+nvfp4_status nvfp4_attention(const nvfp4_attention_args *x, nvfp4_stream_t stream) {
+    if (x == nullptr) return NVFP4_ERR_INVALID_ARG;
+    AttnArgs a;
+    bool empty = false;
+    nvfp4_status st = attention_args(*x, &a, &empty);
+    if (st != NVFP4_OK || empty) return st;
+    st = check_device();
+    if (st != NVFP4_OK) return st;
+    cudaError_t e = launch_attention(a, stream);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    return from_cuda(e);
 }
 
 }  // extern "C"

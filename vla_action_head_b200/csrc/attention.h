@@ -1,0 +1,65 @@
+// attention.h — internal interface between the C ABI (api.cu) and the attention-side kernels
+// (qk_norm_rope.cu, kv_cache.cu, attention.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace nvfp4 {
+
+// A bf16 [B, T, H, D] view (strides in elements).
+struct Heads {
+    uint16_t *ptr;
+    long long sb, st, sh;
+};
+
+// The two planes of an NVFP4 cache tensor: codes [B, H, C, D/2], scales [B, H, C, D/16].
+struct CachePlane {
+    uint8_t *codes, *sf;
+    float g;
+};
+struct Cache {
+    CachePlane k, v;
+    int H, C, length;
+};
+
+struct QkArgs {
+    int B, T, Hq, Hkv, D, R;
+    int inter;  // pairs (2i, 2i + 1) instead of (i, i + R/2)
+    int norm;
+    float eps;
+    Heads q, k, v, q_out, k_out;
+    const uint16_t *q_gamma, *k_gamma;
+    const float *table;
+    int table_rows;
+    const int *positions, *start, *count;
+    int cached;
+    Cache cache;
+    uint32_t *status;
+};
+cudaError_t launch_qk_norm_rope(const QkArgs &a, cudaStream_t s);
+
+struct ReadArgs {
+    int B, L, H, D;
+    const int *start;
+    Heads k_out, v_out;  // ptr NULL: not read
+    Cache cache;
+    uint32_t *status;
+};
+cudaError_t launch_kv_read(const ReadArgs &a, cudaStream_t s);
+
+struct AttnArgs {
+    int B, T, S, Hq, Hkv, D, G;  // G = Hq / Hkv
+    float scale_log2;            // scale * log2(e) (* the key cache's global scale)
+    Heads q, k, v, out;
+    const int *kv_len;
+    const uint8_t *mask;
+    long long mask_stride;
+    int cached;
+    Cache cache;
+};
+cudaError_t launch_attention(const AttnArgs &a, cudaStream_t s);
+cudaError_t probe_attention();
+
+}  // namespace nvfp4

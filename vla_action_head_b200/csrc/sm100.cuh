@@ -17,6 +17,7 @@ enum : uint32_t {
     kStatusTimeoutAccum = 3,    // epilogue waited too long for the accumulator
     kStatusTimeoutDrain = 4,    // teardown waited too long for copies / MMAs in flight
     kStatusTimeoutPeer = 6,     // a split-K partner never delivered its partial
+    kStatusBadIndex = 8,        // a position or cache row that does not exist (no timeout)
 };
 
 // Wall-clock bound of one wait (ns).  Far above any legitimate wait of these kernels.

@@ -56,6 +56,31 @@ class _Program(C.Structure):
                 ("tiles", C.c_int)]
 
 
+class _Heads(C.Structure):
+    _fields_ = [("ptr", C.c_void_p), ("stride_b", C.c_int64), ("stride_t", C.c_int64), ("stride_h", C.c_int64)]
+
+
+class _KVCache(C.Structure):
+    _fields_ = [("k_codes", C.c_void_p), ("k_sf", C.c_void_p), ("v_codes", C.c_void_p), ("v_sf", C.c_void_p),
+                ("k_scale", C.c_float), ("v_scale", C.c_float), ("B", C.c_int), ("H", C.c_int),
+                ("capacity", C.c_int), ("D", C.c_int), ("length", C.c_int)]
+
+
+class _QkArgs(C.Structure):
+    _fields_ = [("B", C.c_int), ("T", C.c_int), ("Hq", C.c_int), ("Hkv", C.c_int), ("D", C.c_int), ("R", C.c_int),
+                ("pairs", C.c_int), ("norm", C.c_int), ("eps", C.c_float), ("q", _Heads), ("k", _Heads),
+                ("v", _Heads), ("q_out", _Heads), ("k_out", _Heads), ("q_gamma", C.c_void_p),
+                ("k_gamma", C.c_void_p), ("table", C.c_void_p), ("table_rows", C.c_int), ("positions", C.c_void_p),
+                ("start", C.c_void_p), ("count", C.c_void_p), ("cache", C.POINTER(_KVCache))]
+
+
+class _AttentionArgs(C.Structure):
+    _fields_ = [("B", C.c_int), ("T", C.c_int), ("S", C.c_int), ("Hq", C.c_int), ("Hkv", C.c_int), ("D", C.c_int),
+                ("scale", C.c_float), ("q", _Heads), ("k", _Heads), ("v", _Heads), ("out", _Heads),
+                ("kv_len", C.c_void_p), ("key_mask", C.c_void_p), ("mask_stride", C.c_int64),
+                ("cache", C.POINTER(_KVCache)), ("workspace", C.c_void_p), ("ws_bytes", C.c_size_t)]
+
+
 _lib = None
 P, I, F, SZ = C.c_void_p, C.c_int, C.c_float, C.c_size_t
 
@@ -92,6 +117,10 @@ def lib():
                                                     P]),
             "nvfp4_gemm": (I, [C.POINTER(_Tensor), C.POINTER(_Tensor), I, I, I, I, P, P, I, P, I, P, P,
                                F, P, SZ, P]),
+            "nvfp4_qk_norm_rope": (I, [C.POINTER(_QkArgs), P]),
+            "nvfp4_kv_read": (I, [C.POINTER(_KVCache), P, I, _Heads, _Heads, P]),
+            "nvfp4_attention": (I, [C.POINTER(_AttentionArgs), P]),
+            "nvfp4_attention_workspace_bytes": (SZ, [C.POINTER(_AttentionArgs)]),
             "nvfp4_program_bytes": (SZ, [I]),
             "nvfp4_program_build": (I, [C.POINTER(_Op), I, P, SZ, C.POINTER(_Program)]),
             "nvfp4_program_run": (I, [C.POINTER(_Program), P]),
@@ -383,3 +412,225 @@ class GroupedGemm:
             return
         for a, w, o, b in self.problems:
             gemm(a, w, self.epi, bias=b, out=o, workspace=self.workspace)
+
+
+# ---- attention side: per-head norm + rotation, the NVFP4 cache, attention -------------------
+# Which tensors a call takes is checked here (types, shapes, device); the library checks the
+# rest (sizes, alignment, strides, ranges).  A call runs on the current stream of its tensors'
+# device.
+PAIRS = {"half": 0, "inter": 1}
+
+
+def rope_table(rows, R, base=10000.0, device="cuda"):
+    """Rotation table fp32 [rows, R] of positions 0 .. rows - 1: cos, then sin, of position *
+    base^(-2i/R), i < R/2; the angles in 64 bits."""
+    torch = _torch()
+    f = float(base) ** (-torch.arange(0, R, 2, dtype=torch.float64, device=device) / R)
+    a = torch.arange(rows, dtype=torch.float64, device=device)[:, None] * f
+    return torch.cat([a.cos(), a.sin()], 1).float()
+
+
+@dataclass
+class KVCache:
+    """An NVFP4 key/value cache (nvfp4_kv_cache): codes uint8 [B, H, capacity, D/2] and scale
+    bytes uint8 [B, H, capacity, D/16] of keys and values, their global scales, and the rows in
+    use (length; all of them if None)."""
+    k_codes: "object"
+    k_sf: "object"
+    v_codes: "object"
+    v_sf: "object"
+    k_scale: float = 1.0
+    v_scale: float = 1.0
+    length: Optional[int] = None
+
+    def c(self):
+        torch = _torch()
+        B, H, cap, d2 = self.k_codes.shape
+        for n, t, w in (("k_codes", self.k_codes, d2), ("k_sf", self.k_sf, d2 // 8),
+                        ("v_codes", self.v_codes, d2), ("v_sf", self.v_sf, d2 // 8)):
+            if t.dtype != torch.uint8 or tuple(t.shape) != (B, H, cap, w) or not t.is_contiguous():
+                raise ValueError(f"{n} must be a dense uint8 tensor of shape {(B, H, cap, w)}")
+            if t.device != self.k_codes.device:
+                raise ValueError(f"{n} is on {t.device}, k_codes on {self.k_codes.device}")
+        return _KVCache(self.k_codes.data_ptr(), self.k_sf.data_ptr(), self.v_codes.data_ptr(),
+                        self.v_sf.data_ptr(), self.k_scale, self.v_scale, B, H, cap, 2 * d2, self.rows())
+
+    def rows(self):
+        return self.k_codes.shape[2] if self.length is None else int(self.length)
+
+
+def empty_kv_cache(B, length, H, D, device="cuda", k_scale=1.0, v_scale=1.0) -> KVCache:
+    """A cache of `length` rows per sequence and head, every row zero."""
+    torch = _torch()
+    cap = (length + 15) // 16 * 16
+    bufs = [torch.zeros((B, H, cap, D // n), dtype=torch.uint8, device=device) for n in (2, 16, 2, 16)]
+    return KVCache(*bufs, k_scale, v_scale, length)
+
+
+def _tensor(name, t, dtype, shape, device):
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    return t
+
+
+def _heads(name, t, shape, device):
+    """A bf16 [B, T, H, D] view, the elements of a head adjacent."""
+    if t is None:
+        raise ValueError(f"{name} is missing")
+    _tensor(name, t, _torch().bfloat16, shape, device)
+    s = t.stride()
+    if shape[3] > 1 and s[3] != 1:
+        raise ValueError(f"{name}: the elements of a head must be adjacent")
+    return _Heads(t.data_ptr(), s[0], s[1], s[2])
+
+
+def _dense(name, t, dtype, shape, device):
+    if t is None:
+        return None
+    if not _tensor(name, t, dtype, shape, device).is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _on(device, fn, *args):
+    """fn(*args, stream) on the current stream of `device`, with that device current."""
+    torch = _torch()
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a CUDA device, not on {device}")
+    if device.index == torch.cuda.current_device():
+        return fn(*args, _stream())
+    with torch.cuda.device(device):
+        return fn(*args, _stream())
+
+
+def qk_norm_rope(q, k, q_gamma=None, k_gamma=None, table=None, positions=None, eps=1e-6, pairs="half", norm=True,
+                 v=None, cache: Optional[KVCache] = None, start=None, count=None, q_out=None, k_out=None):
+    """Per-head RMS norm and rotation of queries q [B, T, Hq, D] and keys k [B, T, Hkv, D] (bf16
+    views; either may be None) in one launch -> (q_out, k_out), new tensors unless given (they
+    may be q and k).
+
+    table: rope_table [rows, R] (None: no rotation), pairs "half" (i, i + R/2) or "inter"
+    (2i, 2i + 1); positions int32 [B, T] (None: start[b] + t); norm=False: no norm.
+    With cache, k and v [B, T, Hkv, D] are quantized into its rows start[b] + t (start int32 [B],
+    None: 0) instead, and the result is (q_out, cache).  count int32 [B]: the tokens of each
+    sequence; the others' outputs and rows are left as they were."""
+    torch = _torch()
+    ref = q if q is not None else k
+    if ref is None:
+        raise ValueError("q and k are both missing")
+    if pairs not in PAIRS:
+        raise ValueError(f"pairs must be 'half' or 'inter', got {pairs!r}")
+    if ref.dim() != 4:
+        raise ValueError(f"q and k must be [B, T, H, D], got {tuple(ref.shape)}")
+    (B, T, _, D), dev = ref.shape, ref.device
+    a = _QkArgs(B=B, T=T, D=D, pairs=PAIRS[pairs], norm=int(bool(norm)), eps=eps)
+    if q is not None:
+        a.Hq = q.shape[2]
+        a.q = _heads("q", q, (B, T, a.Hq, D), dev)
+        if q_out is None:
+            q_out = torch.empty((B, T, a.Hq, D), dtype=torch.bfloat16, device=dev)
+        a.q_out = _heads("q_out", q_out, (B, T, a.Hq, D), dev)
+    if k is not None:
+        if k.dim() != 4:
+            raise ValueError(f"k must be [B, T, H, D], got {tuple(k.shape)}")
+        a.Hkv = k.shape[2]
+        a.k = _heads("k", k, (B, T, a.Hkv, D), dev)
+        if cache is None:
+            if k_out is None:
+                k_out = torch.empty((B, T, a.Hkv, D), dtype=torch.bfloat16, device=dev)
+            a.k_out = _heads("k_out", k_out, (B, T, a.Hkv, D), dev)
+    if cache is not None:
+        if k is None or v is None or k_out is not None:
+            raise ValueError("with a cache, k and v are needed, and there is no k_out")
+        a.v = _heads("v", v, (B, T, a.Hkv, D), dev)
+        if cache.k_codes.device != dev:
+            raise ValueError(f"cache is on {cache.k_codes.device}, not on {dev}")
+        c = cache.c()
+        a.cache = C.pointer(c)
+    elif v is not None:
+        raise ValueError("v is taken with a cache only")
+    a.q_gamma = _dense("q_gamma", q_gamma, torch.bfloat16, (D,), dev)
+    a.k_gamma = _dense("k_gamma", k_gamma, torch.bfloat16, (D,), dev)
+    if table is not None:
+        a.table = _dense("table", table, torch.float32, table.shape, dev)
+        a.table_rows, a.R = table.shape
+    a.positions = _dense("positions", positions, torch.int32, (B, T), dev)
+    a.start = _dense("start", start, torch.int32, (B,), dev)
+    a.count = _dense("count", count, torch.int32, (B,), dev)
+    _check("nvfp4_qk_norm_rope", _on(dev, lib().nvfp4_qk_norm_rope, C.byref(a)))
+    return q_out, (cache if cache is not None else k_out)
+
+
+def kv_write(cache: KVCache, k, v, start=None, count=None) -> KVCache:
+    """Quantizes k, v [B, T, H, D] (bf16 views) into the cache's rows start[b] + t, t < count[b]
+    (start, count int32 [B]; None: 0 and T)."""
+    qk_norm_rope(None, k, norm=False, v=v, cache=cache, start=start, count=count)
+    return cache
+
+
+def kv_read(cache: KVCache, start=None, length=None, k_out=None, v_out=None):
+    """The cache's rows start[b] .. start[b] + length - 1 (start int32 [B], None: 0; length None:
+    all rows) as bf16 (k, v), each [B, length, H, D]."""
+    torch = _torch()
+    c, dev = cache.c(), cache.k_codes.device
+    length = c.length if length is None else length
+    shape = (c.B, length, c.H, c.D)
+    k_out = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k_out is None else k_out
+    v_out = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v_out is None else v_out
+    st = _on(dev, lib().nvfp4_kv_read, C.byref(c), _dense("start", start, torch.int32, (c.B,), dev), length,
+             _heads("k_out", k_out, shape, dev), _heads("v_out", v_out, shape, dev))
+    _check("nvfp4_kv_read", st)
+    return k_out, v_out
+
+
+def attention(q, k=None, v=None, cache: Optional[KVCache] = None, kv_len=None, key_mask=None, scale=None, out=None,
+              workspace: Optional[Workspace] = None):
+    """softmax(scale * q k^T) v -> bf16 [B, T, Hq, D] for queries q [B, T, Hq, D] over keys and
+    values of another length: k, v [B, S, Hkv, D] (bf16 views, Hq a multiple of Hkv) or a cache.
+
+    kv_len int32 [B]: keys of each sequence (None: all rows); key_mask bool or uint8 [B, S]: False
+    leaves a key out.  A query without keys gives 0.  scale defaults to 1/sqrt(D).
+    workspace: scratch, grown on demand; None takes it from the allocator for this call."""
+    torch = _torch()
+    if q.dim() != 4:
+        raise ValueError(f"q must be [B, T, Hq, D], got {tuple(q.shape)}")
+    (B, T, Hq, D), dev = q.shape, q.device
+    a = _AttentionArgs(B=B, T=T, Hq=Hq, D=D, scale=D ** -0.5 if scale is None else scale)
+    a.q = _heads("q", q, (B, T, Hq, D), dev)
+    if cache is not None:
+        if k is not None or v is not None:
+            raise ValueError("keys come from k and v or from a cache, not from both")
+        if cache.k_codes.device != dev:
+            raise ValueError(f"cache is on {cache.k_codes.device}, not on {dev}")
+        c = cache.c()
+        a.S, a.Hkv, a.cache = c.length, c.H, C.pointer(c)
+    else:
+        if k is None or v is None:
+            raise ValueError("k and v, or a cache, are needed")
+        if k.dim() != 4:
+            raise ValueError(f"k must be [B, S, Hkv, D], got {tuple(k.shape)}")
+        a.S, a.Hkv = k.shape[1], k.shape[2]
+        a.k = _heads("k", k, (B, a.S, a.Hkv, D), dev)
+        a.v = _heads("v", v, (B, a.S, a.Hkv, D), dev)
+    if out is None:
+        out = torch.empty((B, T, Hq, D), dtype=torch.bfloat16, device=dev)
+    a.out = _heads("out", out, (B, T, Hq, D), dev)
+    a.kv_len = _dense("kv_len", kv_len, torch.int32, (B,), dev)
+    if key_mask is not None:
+        _tensor("key_mask", key_mask, torch.bool if key_mask.dtype == torch.bool else torch.uint8, (B, a.S), dev)
+        if a.S > 1 and key_mask.stride(1) != 1:
+            raise ValueError("key_mask: the places of a sequence must be adjacent")
+        a.key_mask, a.mask_stride = key_mask.data_ptr(), key_mask.stride(0)
+    need = lib().nvfp4_attention_workspace_bytes(C.byref(a))
+    if need:
+        if workspace is not None:
+            ws, a.ws_bytes = workspace.get(need)
+        else:
+            ws, a.ws_bytes = torch.empty(need, dtype=torch.uint8, device=dev), need
+        a.workspace = ws.data_ptr()
+    _check("nvfp4_attention", _on(dev, lib().nvfp4_attention, C.byref(a)))
+    return out
