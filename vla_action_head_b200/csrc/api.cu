@@ -474,6 +474,45 @@ nvfp4_status check_cache(const nvfp4_kv_cache &c, int B, int H, int D, Cache *ou
     return NVFP4_OK;
 }
 
+// A map over bf16 k or v [d, head, key, sequence] (a broadcast dimension has size 1), 128-byte
+// swizzled boxes of 64 elements x box_rows keys.
+bool make_kv_map(CUtensorMap *m, const Heads &x, int D, int H, int S, int B, int box_rows) {
+    auto fn = encode_fn();
+    if (fn == nullptr) return false;
+    auto dim = [](long long stride, int n) { return static_cast<cuuint64_t>(stride != 0 ? n : 1); };
+    auto str = [](long long stride) { return static_cast<cuuint64_t>(stride != 0 ? 2 * stride : 16); };
+    cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), dim(x.sh, H), static_cast<cuuint64_t>(S), dim(x.sb, B)};
+    cuuint64_t strides[3] = {str(x.sh), str(x.st), str(x.sb)};
+    cuuint32_t box[4] = {64u, 1u, static_cast<cuuint32_t>(box_rows), 1u};
+    cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, x.ptr, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Parts of the key range for the tile kernel: the number of least modelled time (us).
+int attention_splits(const AttnArgs &a) {
+    const int slots = sm_count_cached() * (a.D <= 128 ? 2 : 1);
+    const long long tiles = (static_cast<long long>(a.T) * a.G + 127) / 128 * a.B * a.Hkv;
+    const int keys = (a.S + 127) / 128;
+    int best = 1;
+    double best_cost = 1e300;
+    for (int s = 1; s <= keys && s <= 64 && tiles * (s - 1) < slots; ++s) {
+        const double waves = std::ceil(static_cast<double>(tiles * s) / slots);
+        const double cost = waves * ((keys + s - 1) / s * 1.2 + 3.0) + (s > 1 ? 3.0 + 0.05 * s : 0.0);
+        if (cost < best_cost) {
+            best_cost = cost;
+            best = s;
+        }
+    }
+    return best;
+}
+
+size_t attention_workspace(const AttnArgs &a) {
+    if (a.splits <= 1) return 0;
+    return static_cast<size_t>(a.B) * a.T * a.Hq * a.splits * (a.D + 2) * sizeof(float);
+}
+
 // The arguments of nvfp4_attention, without device access; `empty`: there is nothing to write.
 nvfp4_status attention_args(const nvfp4_attention_args &x, AttnArgs *a, bool *empty) {
     if (x.B < 0 || x.T < 0 || x.S < 0 || x.Hq <= 0 || x.Hkv <= 0 || x.D <= 0) return NVFP4_ERR_INVALID_ARG;
@@ -494,6 +533,8 @@ nvfp4_status attention_args(const nvfp4_attention_args &x, AttnArgs *a, bool *em
     if (st == NVFP4_OK && x.cache == nullptr && x.S > 0) {
         st = check_heads(x.k, x.B, x.S, x.Hkv, x.D, false, &a->k);
         if (st == NVFP4_OK) st = check_heads(x.v, x.B, x.S, x.Hkv, x.D, false, &a->v);
+        // keys that share one row are not a cache of keys
+        if (st == NVFP4_OK && x.S > 1 && (a->k.st == 0 || a->v.st == 0)) st = NVFP4_ERR_INVALID_ARG;
     }
     if (st != NVFP4_OK) return st;
     if (x.key_mask != nullptr && (x.mask_stride < 0 || (x.B > 1 && x.mask_stride != 0 && x.mask_stride < x.S)))
@@ -512,6 +553,11 @@ nvfp4_status attention_args(const nvfp4_attention_args &x, AttnArgs *a, bool *em
     a->kv_len = x.kv_len;
     a->mask = x.key_mask;
     a->mask_stride = x.B > 1 ? x.mask_stride : 0;
+    a->k_mul_h = a->k.sh != 0;
+    a->k_mul_b = a->k.sb != 0;
+    a->v_mul_h = a->v.sh != 0;
+    a->v_mul_b = a->v.sb != 0;
+    a->splits = a->cached ? 1 : attention_splits(*a);
     return NVFP4_OK;
 }
 
@@ -525,7 +571,8 @@ nvfp4_status nvfp4_probe(void) {
     // the kernels of this library must load on the device
     if (probe_norm_kernels() != cudaSuccess || probe_gemm_kernels() != cudaSuccess ||
         probe_gemm_persistent() != cudaSuccess ||
-        probe_gemm_grouped() != cudaSuccess || probe_attention() != cudaSuccess) {
+        probe_gemm_grouped() != cudaSuccess || probe_attention() != cudaSuccess ||
+        probe_attention_tiles() != cudaSuccess) {
         cudaGetLastError();
         return NVFP4_ERR_UNSUPPORTED_DEVICE;
     }
@@ -1020,8 +1067,10 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache *cache, const int32_t *start, in
 }
 
 size_t nvfp4_attention_workspace_bytes(const nvfp4_attention_args *x) {
-    (void)x;
-    return 0;
+    AttnArgs a;
+    bool empty = false;
+    if (x == nullptr || attention_args(*x, &a, &empty) != NVFP4_OK || empty) return 0;
+    return attention_workspace(a);
 }
 
 nvfp4_status nvfp4_attention(const nvfp4_attention_args *x, nvfp4_stream_t stream) {
@@ -1030,9 +1079,27 @@ nvfp4_status nvfp4_attention(const nvfp4_attention_args *x, nvfp4_stream_t strea
     bool empty = false;
     nvfp4_status st = attention_args(*x, &a, &empty);
     if (st != NVFP4_OK || empty) return st;
+    const size_t need = attention_workspace(a);
+    if (need > 0) {
+        if (x->workspace == nullptr || x->ws_bytes < need) return NVFP4_ERR_WORKSPACE;
+        if (!aligned16(x->workspace)) return NVFP4_ERR_MISALIGNED;
+        a.part_o = static_cast<float *>(x->workspace);
+        a.part_ml = reinterpret_cast<float2 *>(a.part_o + static_cast<size_t>(a.B) * a.T * a.Hq * a.splits * a.D);
+    }
     st = check_device();
     if (st != NVFP4_OK) return st;
-    cudaError_t e = launch_attention(a, stream);
+    if ((a.status = status_word()) == nullptr) return NVFP4_ERR_CUDA;
+    cudaError_t e;
+    if (a.cached || a.S == 0) {
+        e = launch_attention(a, stream);
+    } else {
+        CUtensorMap mk, mv;
+        if (!make_kv_map(&mk, a.k, a.D, a.Hkv, a.S, a.B, 128) ||
+            !make_kv_map(&mv, a.v, a.D, a.Hkv, a.S, a.B, attention_v_box_rows(a.D)))
+            return NVFP4_ERR_CUDA;
+        e = launch_attention_tiles(mk, mv, a, stream);
+        if (e == cudaSuccess && a.splits > 1) e = launch_attention_join(a, stream);
+    }
     if (e == cudaSuccess) e = cudaGetLastError();
     return from_cuda(e);
 }

@@ -2,6 +2,7 @@
 // (qk_norm_rope.cu, kv_cache.cu, attention.cu).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -58,8 +59,20 @@ struct AttnArgs {
     long long mask_stride;
     int cached;
     Cache cache;
+    int k_mul_h, k_mul_b, v_mul_h, v_mul_b;  // 0: that dimension is broadcast, its tensor-map size 1
+    int splits;      // parts of the key range; > 1: joined from part_o and part_ml
+    float *part_o;   // [rows of all heads, splits, D]: unnormalized sums
+    float2 *part_ml; // [rows of all heads, splits]: reference, sum of weights
+    uint32_t *status;
 };
 cudaError_t launch_attention(const AttnArgs &a, cudaStream_t s);
+cudaError_t launch_attention_join(const AttnArgs &a, cudaStream_t s);
 cudaError_t probe_attention();
+
+// Tensor-core tiles of 128 rows x 128 keys; maps over k and v [d, head, key, sequence] with boxes of
+// 64 x 1 x 128 x 1 and 64 x 1 x attention_v_box_rows x 1 elements.
+int attention_v_box_rows(int D);
+cudaError_t launch_attention_tiles(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a, cudaStream_t s);
+cudaError_t probe_attention_tiles();
 
 }  // namespace nvfp4

@@ -1,0 +1,471 @@
+// attention_tiles.cu — attention in tiles of 128 query rows x 128 keys on the tensor cores.
+//
+//   S = Q K^T (fp32, tensor memory);  p = 2^(c S - c m) with the running reference m;
+//   l = sum p;  O += P V;  out = O / l,                  c = scale log2(e)
+//
+// The rows of a tile are the (query, head) pairs that share a key head, query-major, so a group of
+// G heads reads its keys once.  One CTA takes one row tile and a range of key tiles (the whole
+// sequence, or one of `splits` parts whose O, m and l are joined by attention_join_kernel).
+//
+// Roles (192 threads): warp 5 brings K and V through a ring of 16 KB chunks by TMA (a K chunk is 128
+// keys x 64 elements, a V chunk all elements of 16384 / (2 DP) keys: both are what one step of
+// the MMA loop eats), warp 4 issues the MMAs, warps 0-3 own a row a thread: scores from tensor
+// memory, softmax, P back to tensor memory as the A operand of P V, where it overwrites its own
+// scores.  With 256-wide heads O takes half of the tensor memory and two score tiles the rest, so
+// Q K^T of the next tile runs under the softmax of this one; narrower heads keep one score tile
+// and half of the tensor and shared memory, and two CTAs share an SM and fill each other's gaps.
+//
+// O is rescaled only where the row maximum outgrew the reference by more than 2^8 (the weights
+// stay below 2^8, l and O are fp32; the final division cancels the reference).
+//
+// Left-out keys: their scores become -inf whatever they hold, and their V rows are zeroed in
+// shared memory before the product, as 0 x inf is not 0.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "attention.h"
+#include "gemm.h"
+#include "quant.cuh"
+#include "sm100.cuh"
+
+namespace nvfp4 {
+
+namespace {
+
+constexpr int kThreads = 192;
+constexpr int kChunk = 16384;
+constexpr float kLazy = 8.0f;  // log2 of the growth of the maximum that forces a rescale
+
+template <int DP>
+struct Cfg {
+    static constexpr int kScores = DP == 256 ? 2 : 1;    // score tiles in tensor memory
+    static constexpr int kRing = DP == 256 ? 10 : 5;     // chunks
+    static constexpr int kVC = DP / 64;                  // V chunks of a tile
+    static constexpr int kKeysPerV = 128 / kVC;          // keys of a V chunk
+    static constexpr int kQBytes = 128 * DP * 2;
+    static constexpr int kOffRing = kQBytes;
+    static constexpr int kOffBar = kOffRing + kRing * kChunk;
+    // full[kRing], empty[kRing], s_full[2], p_ready, o_done
+    static constexpr int kOffMisc = kOffBar + (2 * kRing + 4) * 8;
+    static constexpr int kSmem = kOffMisc + 16;
+    static constexpr int kTmemCols = DP == 256 ? 512 : 256;
+    static constexpr int kColS = DP == 256 ? 256 : 128;  // O at 0, then the score tiles
+    static constexpr int kCtas = DP == 256 ? 1 : 2;      // per SM
+};
+static_assert(Cfg<256>::kSmem <= 232448 && 2 * (Cfg<128>::kSmem + 1024) <= 233472, "shared memory");
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Ring positions of a tile's first K and V chunk.  The MMA loop's order is K0 K1 V0 K2 V1 ... with
+// two score tiles, K0 V0 K1 V1 ... with one.
+template <int SCORES>
+__device__ __forceinline__ int k_pos(int i, int kc, int vc) {
+    if constexpr (SCORES == 1) return i * (kc + vc);
+    return i == 0 ? 0 : kc + (i - 1) * (kc + vc);
+}
+template <int SCORES>
+__device__ __forceinline__ int v_pos(int i, int n, int kc, int vc) {
+    if constexpr (SCORES == 1) return i * (kc + vc) + kc;
+    return i < n - 1 ? 2 * kc + i * (kc + vc) : n * kc + i * vc;
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
+    attention_tiles_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                           const AttnArgs p) {
+    using C = Cfg<DP>;
+    extern __shared__ __align__(1024) uint8_t smem[];  // 128-byte swizzle atoms
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t bar_full = sbase + C::kOffBar, bar_empty = bar_full + 8 * C::kRing;
+    const uint32_t bar_s = bar_empty + 8 * C::kRing, bar_p = bar_s + 16, bar_o = bar_p + 8;
+    volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(smem + C::kOffMisc);  // TMEM base, abort
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    // the CTA's place: split fastest, then row tile, key head, sequence
+    int rest = static_cast<int>(blockIdx.x);
+    const int split = rest % p.splits;
+    rest /= p.splits;
+    const int rows = p.T * p.G;
+    const int row_tiles = (rows + 127) >> 7;
+    const int row0 = (rest % row_tiles) << 7;
+    rest /= row_tiles;
+    const int hk = rest % p.Hkv, b = rest / p.Hkv;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kRing; ++i) {
+            mbar_init(bar_full + 8 * i, 1);
+            mbar_init(bar_empty + 8 * i, 1);
+        }
+        mbar_init(bar_s, 1);
+        mbar_init(bar_s + 8, 1);
+        mbar_init(bar_p, 128);
+        mbar_init(bar_o, 1);
+        misc[1] = 0;
+        fence_mbar_init();
+    }
+    if (warp == 4) {
+        tmem_alloc(smem_u32(const_cast<uint32_t *>(misc)), C::kTmemCols);
+        tmem_relinquish();
+    }
+    pdl_launch_dependents();
+    pdl_wait();  // q, k, v and kv_len may come from the previous kernel
+    int len = p.S;
+    if (p.kv_len != nullptr) len = min(max(__ldg(p.kv_len + b), 0), p.S);
+    const int all_tiles = (len + 127) >> 7, per = (all_tiles + p.splits - 1) / p.splits;
+    const int tile0 = split * per, n = max(0, min(per, all_tiles - tile0));
+    const int kc = (p.D + 63) >> 6;  // 64-element blocks of a head
+    constexpr int vc = C::kVC;
+
+    if (warp < 4) {
+        // Q rows into K-major swizzled tiles (zeros past D and past the last row)
+        constexpr int kUnits = DP / 8;
+        for (int u = threadIdx.x; u < 128 * kUnits; u += 128) {
+            const int r = u / kUnits, c = u % kUnits, row = row0 + r;
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (row < rows && 8 * c < p.D) {
+                const int t = row / p.G, h = hk * p.G + row % p.G;
+                v = __ldcg(reinterpret_cast<const uint4 *>(p.q.ptr + b * p.q.sb + t * p.q.st + h * p.q.sh + 8 * c));
+            }
+            *reinterpret_cast<uint4 *>(smem + (c >> 3) * kChunk + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+        }
+        fence_proxy_async_smem();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = misc[0];
+
+    if (warp == 5) {
+        if (lane == 0) {
+            // ------------------------------ producer ------------------------------
+            const uint64_t pol = policy_evict_last();
+            int pos = 0;
+            bool ok = true;
+            auto take = [&](uint32_t bytes) -> uint32_t {  // the next chunk, free and expecting `bytes`
+                const int slot = pos % C::kRing, use = pos / C::kRing;
+                if (use > 0) ok = ok && mbar_wait(bar_empty + 8 * slot, (use - 1) & 1, abort_flag, p.status,
+                                                  kStatusTimeoutEmpty);
+                if (ok) mbar_arrive_expect_tx(bar_full + 8 * slot, bytes);
+                return static_cast<uint32_t>(slot);
+            };
+            const int zh = p.k_mul_h * hk, zb = p.k_mul_b * b, vh = p.v_mul_h * hk, vb = p.v_mul_b * b;
+            auto load_k = [&](int i) {
+                for (int c = 0; c < kc && ok; ++c, ++pos) {
+                    const uint32_t slot = take(kChunk);
+                    if (!ok) break;
+                    tma_load_4d(sbase + C::kOffRing + slot * kChunk, &map_k, 64 * c, zh, (tile0 + i) << 7, zb,
+                                bar_full + 8 * slot, pol);
+                }
+            };
+            auto load_v = [&](int i) {
+                for (int c = 0; c < vc && ok; ++c, ++pos) {
+                    const uint32_t slot = take(kc * C::kKeysPerV * 128);
+                    if (!ok) break;
+                    for (int e = 0; e < kc; ++e)
+                        tma_load_4d(sbase + C::kOffRing + slot * kChunk + e * C::kKeysPerV * 128, &map_v, 64 * e, vh,
+                                    ((tile0 + i) << 7) + c * C::kKeysPerV, vb, bar_full + 8 * slot, pol);
+                }
+            };
+            if (n > 0) load_k(0);
+            for (int i = 0; i < n && ok; ++i) {
+                if (C::kScores == 2 && i + 1 < n) load_k(i + 1);
+                load_v(i);
+                if (C::kScores == 1 && i + 1 < n) load_k(i + 1);
+            }
+            // leave no copy in flight behind
+            int dummy = 0;
+            for (int q = max(0, pos - C::kRing); q < pos; ++q)
+                mbar_wait(bar_full + 8 * (q % C::kRing), (q / C::kRing) & 1, &dummy, p.status, kStatusTimeoutDrain);
+        }
+    } else if (warp == 4) {
+        if (lane == 0 && n > 0) {
+            // ------------------------------ MMA issuer ------------------------------
+            constexpr uint32_t idesc_s = idesc_f16(128, 128, true, false);
+            const uint32_t idesc_o = idesc_f16(128, (p.D + 15) & ~15, true, true);
+            const int ksteps = (p.D + 15) >> 4;
+            bool ok = true;
+            auto full = [&](int pos) {
+                ok = ok && mbar_wait(bar_full + 8 * (pos % C::kRing), (pos / C::kRing) & 1, abort_flag, p.status,
+                                     kStatusTimeoutFull);
+                tc_fence_after();
+                return sbase + C::kOffRing + (pos % C::kRing) * kChunk;
+            };
+            auto qk = [&](int i) {
+                const int pos = k_pos<C::kScores>(i, kc, vc), buf = i % C::kScores;
+                const uint32_t d = tmem + C::kColS + buf * 128;
+                for (int c = 0; c < kc && ok; ++c) {
+                    const uint32_t kb = full(pos + c);
+                    if (!ok) break;
+                    for (int k = 4 * c; k < min(4 * c + 4, ksteps); ++k)
+                        tc_mma_f16_ss(d, desc_kmajor_sw128(sbase + c * kChunk + 32 * (k & 3)),
+                                      desc_kmajor_sw128(kb + 32 * (k & 3)), idesc_s, k > 0 ? 1u : 0u);
+                    tc_commit(bar_empty + 8 * ((pos + c) % C::kRing));
+                }
+                tc_commit(bar_s + 8 * buf);
+            };
+            qk(0);
+            for (int i = 0; i < n && ok; ++i) {
+                if (C::kScores == 2 && i + 1 < n) qk(i + 1);
+                ok = ok && mbar_wait(bar_p, i & 1, abort_flag, p.status, kStatusTimeoutSoftmax);
+                if (!ok) break;
+                tc_fence_after();
+                const int pos = v_pos<C::kScores>(i, n, kc, vc);
+                const uint32_t pt = tmem + C::kColS + (i % C::kScores) * 128;
+                for (int c = 0; c < vc && ok; ++c) {
+                    const uint32_t v = full(pos + c);
+                    if (!ok) break;
+                    constexpr int steps = C::kKeysPerV / 16;
+                    for (int k = 0; k < steps; ++k)
+                        tc_mma_f16_ts(tmem, pt + 8 * (c * steps + k), desc_mnmajor_sw128(v + 2048 * k, C::kKeysPerV * 128),
+                                      idesc_o, (i > 0 || c > 0 || k > 0) ? 1u : 0u);
+                    tc_commit(bar_empty + 8 * ((pos + c) % C::kRing));
+                }
+                tc_commit(bar_o);
+                if (C::kScores == 1 && i + 1 < n) qk(i + 1);
+            }
+        }
+    } else {
+        // ------------------------------ softmax, a row a thread ------------------------------
+        const int row = row0 + threadIdx.x;
+        const bool warp_on = row0 + warp * 32 < rows;  // some row of this warp exists
+        const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+        const float c = p.scale_log2;
+        float m = -INFINITY, l = 0.0f;
+        bool ok = true;
+        for (int i = 0; i < n; ++i) {
+            ok = mbar_wait(bar_s + 8 * (i % C::kScores), (i / C::kScores) & 1, abort_flag, p.status,
+                           kStatusTimeoutAccum);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            const int j0 = (tile0 + i) << 7;
+            const bool part = p.mask != nullptr || j0 + 128 > len;
+            uint32_t keep[4];
+            if (part) {
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const int j = j0 + 32 * w + lane;
+                    bool in = j < len;
+                    if (in && p.mask != nullptr) in = __ldg(p.mask + b * p.mask_stride + j) != 0;
+                    keep[w] = __ballot_sync(0xffffffffu, in);
+                }
+            }
+            if (warp_on) {
+                const uint32_t ts = lane_base + C::kColS + (i % C::kScores) * 128;
+                // the scores stay in registers where a thread may have 255, else they are read twice
+                constexpr bool kKeep = C::kCtas == 1;
+                uint32_t s[kKeep ? 4 : 2][32];
+                auto load = [&](uint32_t (&x)[32], int w) { tmem_ld_32x32b_x32(ts + 32 * w, x); };
+                auto leave_out = [&](uint32_t (&x)[32], int w) {
+                    if (part) {
+                        const uint32_t k = w == 0 ? keep[0] : w == 1 ? keep[1] : w == 2 ? keep[2] : keep[3];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (((k >> j) & 1u) == 0u) x[j] = 0xFF800000u;
+                    }
+                };
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                auto top_of = [&](const uint32_t (&x)[32]) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(x[j]));
+                };
+                if constexpr (kKeep) {
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) load(s[w], w);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        leave_out(s[w], w);
+                        top_of(s[w]);
+                    }
+                } else {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        load(s[0], 2 * half);
+                        load(s[1], 2 * half + 1);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int w = 0; w < 2; ++w) {
+                            leave_out(s[w], 2 * half + w);
+                            top_of(s[w]);
+                        }
+                    }
+                }
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                // the reference: the first maximum, then only one that outgrew it
+                const bool grow = top > m && !((top - m) * c <= kLazy);
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float f = grow ? ex2((m - top) * c) : 1.0f;
+                    if (grow) m = top;
+                    if (i > 0) {
+                        ok = mbar_wait(bar_o, (i - 1) & 1, abort_flag, p.status, kStatusTimeoutAccum);
+                        if (!__all_sync(0xffffffffu, ok)) break;
+                        tc_fence_after();
+                        l *= f;
+                        for (int e = 0; e < p.D; e += 32) {
+                            uint32_t o[32];
+                            tmem_ld_32x32b_x32(lane_base + e, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                            tmem_st_32x32b_x32(lane_base + e, o);
+                        }
+                    }
+                }
+                const float mc = m == -INFINITY ? 0.0f : m * c;
+                float sum[4] = {};
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t pk[32];
+                    if constexpr (!kKeep) {  // P of this half overwrites scores already read
+                        load(s[0], 2 * half);
+                        load(s[1], 2 * half + 1);
+                        tmem_ld_wait();
+                        leave_out(s[0], 2 * half);
+                        leave_out(s[1], 2 * half + 1);
+                    }
+#pragma unroll
+                    for (int w = 0; w < 2; ++w)
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            const uint32_t *sw = s[kKeep ? 2 * half + w : w];
+                            const float x = ex2(fmaf(__uint_as_float(sw[j]), c, -mc));
+                            const float y = ex2(fmaf(__uint_as_float(sw[j + 1]), c, -mc));
+                            sum[2 * w] += x;
+                            sum[2 * w + 1] += y;
+                            pk[16 * w + j / 2] = pack_bf16x2_rn(x, y);
+                        }
+                    tmem_st_32x32b_x32(ts + 32 * half, pk);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tmem_st_wait();
+            }
+            if (part) {
+                // this thread's key row of V: zeros if the key is left out.  Once the previous product is
+                // done every chunk before V's has landed, so the phase waited for is V's own.
+                if (((keep[warp] >> lane) & 1u) == 0u) {
+                    if (i > 0) ok = mbar_wait(bar_o, (i - 1) & 1, abort_flag, p.status, kStatusTimeoutAccum);
+                    const int key = threadIdx.x, pos = v_pos<C::kScores>(i, n, kc, vc) + key / C::kKeysPerV;
+                    ok = ok && mbar_wait(bar_full + 8 * (pos % C::kRing), (pos / C::kRing) & 1, abort_flag,
+                                         p.status, kStatusTimeoutFull);
+                    uint8_t *v = smem + C::kOffRing + (pos % C::kRing) * kChunk + (key % C::kKeysPerV) * 128;
+                    if (ok)
+                        for (int e = 0; e < kc; ++e)
+#pragma unroll
+                            for (int q = 0; q < 8; ++q)
+                                *reinterpret_cast<uint4 *>(v + e * C::kKeysPerV * 128 + ((q ^ (lane & 7)) << 4)) =
+                                    make_uint4(0u, 0u, 0u, 0u);
+                    fence_proxy_async_smem();
+                }
+                if (!__all_sync(0xffffffffu, ok)) break;
+            }
+            tc_fence_before();
+            mbar_arrive(bar_p);
+        }
+
+        // ------------------------------ output ------------------------------
+        // (the product before the last may still run: wait for each in turn)
+        for (int i = max(0, n - 2); i < n; ++i)
+            ok = ok && mbar_wait(bar_o, i & 1, abort_flag, p.status, kStatusTimeoutAccum);
+        tc_fence_after();
+        if (__all_sync(0xffffffffu, ok) && warp_on) {
+            const bool on = row < rows;
+            const int t = row / p.G, h = hk * p.G + row % p.G;
+            const float f = l != 0.0f ? 1.0f / l : 0.0f;
+            if (p.splits > 1) {
+                const size_t at = ((static_cast<size_t>(b) * p.Hkv + hk) * rows + row) * p.splits + split;
+                if (on) p.part_ml[at] = make_float2(m, l);
+                for (int e = 0; e < p.D && n > 0; e += 32) {
+                    uint32_t o[32];
+                    tmem_ld_32x32b_x32(lane_base + e, o);
+                    tmem_ld_wait();
+                    float4 *to = reinterpret_cast<float4 *>(p.part_o + at * p.D + e);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (on && e + 4 * j < p.D)
+                            to[j] = make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]),
+                                                __uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 3]));
+                }
+            } else {
+                uint16_t *to = p.out.ptr + b * p.out.sb + t * p.out.st + h * p.out.sh;
+                for (int e = 0; e < p.D; e += 32) {
+                    uint32_t o[32];
+                    tmem_ld_32x32b_x32(lane_base + e, o);
+                    tmem_ld_wait();
+                    if (l == 0.0f) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = 0u;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            w[q] = pack_bf16x2_rn(__uint_as_float(o[8 * j + 2 * q]) * f,
+                                                  __uint_as_float(o[8 * j + 2 * q + 1]) * f);
+                        if (on && e + 8 * j < p.D)
+                            *reinterpret_cast<uint4 *>(to + e + 8 * j) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            }
+        }
+    }
+
+    // teardown
+    __syncwarp();
+    if (*abort_flag) {
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 200000ull) {
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 4) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::kTmemCols);
+    }
+}
+
+template <int DP>
+cudaError_t launch_dp(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a, cudaStream_t s) {
+    using C = Cfg<DP>;
+    static std::atomic<bool> attr_set[kMaxDevices];
+    auto *kernel = attention_tiles_kernel<DP>;
+    cudaError_t e = set_smem_limit_once(reinterpret_cast<const void *>(kernel), C::kSmem, attr_set);
+    if (e != cudaSuccess) return e;
+    const long long tiles = (static_cast<long long>(a.T) * a.G + 127) / 128;
+    const long long ctas = tiles * a.B * a.Hkv * a.splits;
+    if (ctas > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_enabled() ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, mk, mv, a);
+}
+
+}  // namespace
+
+int attention_v_box_rows(int D) { return D <= 64 ? 128 : D <= 128 ? 64 : 32; }
+
+cudaError_t launch_attention_tiles(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a, cudaStream_t s) {
+    if (a.D <= 64) return launch_dp<64>(mk, mv, a, s);
+    if (a.D <= 128) return launch_dp<128>(mk, mv, a, s);
+    return launch_dp<256>(mk, mv, a, s);
+}
+
+cudaError_t probe_attention_tiles() {
+    cudaFuncAttributes fa;
+    return cudaFuncGetAttributes(&fa, attention_tiles_kernel<256>);
+}
+
+}  // namespace nvfp4
