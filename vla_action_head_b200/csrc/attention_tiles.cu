@@ -45,8 +45,8 @@ struct Cfg {
     static constexpr int kQBytes = 128 * DP * 2;
     static constexpr int kOffRing = kQBytes;
     static constexpr int kOffBar = kOffRing + kRing * kChunk;
-    // full[kRing], empty[kRing], s_full[2], p_ready, o_done
-    static constexpr int kOffMisc = kOffBar + (2 * kRing + 4) * 8;
+    // full[kRing], empty[kRing], s_full[2], p_ready, o_done, all_done
+    static constexpr int kOffMisc = kOffBar + (2 * kRing + 5) * 8 + 8;
     static constexpr int kSmem = kOffMisc + 16;
     static constexpr int kTmemCols = DP == 256 ? 512 : 256;
     static constexpr int kColS = DP == 256 ? 256 : 128;  // O at 0, then the score tiles
@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
     extern __shared__ __align__(1024) uint8_t smem[];  // 128-byte swizzle atoms
     const uint32_t sbase = smem_u32(smem);
     const uint32_t bar_full = sbase + C::kOffBar, bar_empty = bar_full + 8 * C::kRing;
-    const uint32_t bar_s = bar_empty + 8 * C::kRing, bar_p = bar_s + 16, bar_o = bar_p + 8;
+    const uint32_t bar_s = bar_empty + 8 * C::kRing, bar_p = bar_s + 16, bar_o = bar_p + 8, bar_all = bar_o + 8;
     volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(smem + C::kOffMisc);  // TMEM base, abort
     volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
         mbar_init(bar_s + 8, 1);
         mbar_init(bar_p, 128);
         mbar_init(bar_o, 1);
+        mbar_init(bar_all, 1);
         misc[1] = 0;
         fence_mbar_init();
     }
@@ -225,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
                                       idesc_o, (i > 0 || c > 0 || k > 0) ? 1u : 0u);
                     tc_commit(bar_empty + 8 * ((pos + c) % C::kRing));
                 }
-                tc_commit(bar_o);
+                tc_commit(i + 1 < n ? bar_o : bar_all);
                 if (C::kScores == 1 && i + 1 < n) qk(i + 1);
             }
         }
@@ -368,9 +369,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
         }
 
         // ------------------------------ output ------------------------------
-        // (the product before the last may still run: wait for each in turn)
-        for (int i = max(0, n - 2); i < n; ++i)
-            ok = ok && mbar_wait(bar_o, i & 1, abort_flag, p.status, kStatusTimeoutAccum);
+        // (on a barrier of its own: the one before the last may still be running, or have been done long ago)
+        if (ok && n > 0) ok = mbar_wait(bar_all, 0, abort_flag, p.status, kStatusTimeoutAccum);
         tc_fence_after();
         if (__all_sync(0xffffffffu, ok) && warp_on) {
             const bool on = row < rows;
