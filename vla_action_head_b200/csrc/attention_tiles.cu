@@ -45,8 +45,8 @@ struct Cfg {
     static constexpr int kQBytes = 128 * DP * 2;
     static constexpr int kOffRing = kQBytes;
     static constexpr int kOffBar = kOffRing + kRing * kChunk;
-    // full[kRing], empty[kRing], s_full[2], p_ready, o_done, all_done
-    static constexpr int kOffMisc = kOffBar + (2 * kRing + 5) * 8 + 8;
+    // full[kRing], empty[kRing], s_full[2], p_ready, o_done, all_done, q_ready
+    static constexpr int kOffMisc = kOffBar + (2 * kRing + 6) * 8;
     static constexpr int kSmem = kOffMisc + 16;
     static constexpr int kTmemCols = DP == 256 ? 512 : 256;
     static constexpr int kColS = DP == 256 ? 256 : 128;  // O at 0, then the score tiles
@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
     extern __shared__ __align__(1024) uint8_t smem[];  // 128-byte swizzle atoms
     const uint32_t sbase = smem_u32(smem);
     const uint32_t bar_full = sbase + C::kOffBar, bar_empty = bar_full + 8 * C::kRing;
-    const uint32_t bar_s = bar_empty + 8 * C::kRing, bar_p = bar_s + 16, bar_o = bar_p + 8, bar_all = bar_o + 8;
+    const uint32_t bar_s = bar_empty + 8 * C::kRing, bar_p = bar_s + 16, bar_o = bar_p + 8, bar_all = bar_o + 8, bar_q = bar_all + 8;
     volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(smem + C::kOffMisc);  // TMEM base, abort
     volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -106,6 +106,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
         mbar_init(bar_p, 128);
         mbar_init(bar_o, 1);
         mbar_init(bar_all, 1);
+        mbar_init(bar_q, 128);
         misc[1] = 0;
         fence_mbar_init();
     }
@@ -113,6 +114,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
         tmem_alloc(smem_u32(const_cast<uint32_t *>(misc)), C::kTmemCols);
         tmem_relinquish();
     }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = misc[0];
     pdl_launch_dependents();
     pdl_wait();  // q, k, v and kv_len may come from the previous kernel
     int len = p.S;
@@ -122,27 +127,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
     const int kc = (p.D + 63) >> 6;  // 64-element blocks of a head
     constexpr int vc = C::kVC;
 
-    if (warp < 4) {
-        // Q rows into K-major swizzled tiles (zeros past D and past the last row)
-        constexpr int kUnits = DP / 8;
-        for (int u = threadIdx.x; u < 128 * kUnits; u += 128) {
-            const int r = u / kUnits, c = u % kUnits, row = row0 + r;
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (row < rows && 8 * c < p.D) {
-                const int t = row / p.G, h = hk * p.G + row % p.G;
-                v = __ldcg(reinterpret_cast<const uint4 *>(p.q.ptr + b * p.q.sb + t * p.q.st + h * p.q.sh + 8 * c));
-            }
-            *reinterpret_cast<uint4 *>(smem + (c >> 3) * kChunk + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
-        }
-        fence_proxy_async_smem();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = misc[0];
-
     if (warp == 5) {
-        if (lane == 0) {
+        if (elect_one()) {
             // ------------------------------ producer ------------------------------
             const uint64_t pol = policy_evict_last();
             int pos = 0;
@@ -184,12 +170,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
                 mbar_wait(bar_full + 8 * (q % C::kRing), (q / C::kRing) & 1, &dummy, p.status, kStatusTimeoutDrain);
         }
     } else if (warp == 4) {
-        if (lane == 0 && n > 0) {
+        if (n > 0 && elect_one()) {
             // ------------------------------ MMA issuer ------------------------------
             constexpr uint32_t idesc_s = idesc_f16(128, 128, true, false);
             const uint32_t idesc_o = idesc_f16(128, (p.D + 15) & ~15, true, true);
             const int ksteps = (p.D + 15) >> 4;
-            bool ok = true;
+            bool ok = mbar_wait(bar_q, 0, abort_flag, p.status, kStatusTimeoutFull);
             auto full = [&](int pos) {
                 ok = ok && mbar_wait(bar_full + 8 * (pos % C::kRing), (pos / C::kRing) & 1, abort_flag, p.status,
                                      kStatusTimeoutFull);
@@ -199,12 +185,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
             auto qk = [&](int i) {
                 const int pos = k_pos<C::kScores>(i, kc, vc), buf = i % C::kScores;
                 const uint32_t d = tmem + C::kColS + buf * 128;
+                uint32_t on = 0u;
                 for (int c = 0; c < kc && ok; ++c) {
                     const uint32_t kb = full(pos + c);
                     if (!ok) break;
-                    for (int k = 4 * c; k < min(4 * c + 4, ksteps); ++k)
-                        tc_mma_f16_ss(d, desc_kmajor_sw128(sbase + c * kChunk + 32 * (k & 3)),
-                                      desc_kmajor_sw128(kb + 32 * (k & 3)), idesc_s, k > 0 ? 1u : 0u);
+                    // a step of 16 elements is 32 bytes on: 2 in the descriptors' address field
+                    const uint64_t qd = desc_kmajor_sw128(sbase + c * kChunk), kd = desc_kmajor_sw128(kb);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (4 * c + k < ksteps) {
+                            tc_mma_f16_ss(d, qd + 2 * k, kd + 2 * k, idesc_s, on);
+                            on = 1u;
+                        }
                     tc_commit(bar_empty + 8 * ((pos + c) % C::kRing));
                 }
                 tc_commit(bar_s + 8 * buf);
@@ -217,13 +209,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
                 tc_fence_after();
                 const int pos = v_pos<C::kScores>(i, n, kc, vc);
                 const uint32_t pt = tmem + C::kColS + (i % C::kScores) * 128;
-                for (int c = 0; c < vc && ok; ++c) {
+                uint32_t on = i > 0 ? 1u : 0u;
+#pragma unroll
+                for (int c = 0; c < vc; ++c) {
                     const uint32_t v = full(pos + c);
                     if (!ok) break;
+                    const uint64_t vd = desc_mnmajor_sw128(v, C::kKeysPerV * 128);
                     constexpr int steps = C::kKeysPerV / 16;
-                    for (int k = 0; k < steps; ++k)
-                        tc_mma_f16_ts(tmem, pt + 8 * (c * steps + k), desc_mnmajor_sw128(v + 2048 * k, C::kKeysPerV * 128),
-                                      idesc_o, (i > 0 || c > 0 || k > 0) ? 1u : 0u);
+#pragma unroll
+                    for (int k = 0; k < steps; ++k) {  // 16 keys: 2048 bytes of V, 8 columns of P
+                        tc_mma_f16_ts(tmem, pt + 8 * (c * steps + k), vd + 128 * k, idesc_o, on);
+                        on = 1u;
+                    }
                     tc_commit(bar_empty + 8 * ((pos + c) % C::kRing));
                 }
                 tc_commit(i + 1 < n ? bar_o : bar_all);
@@ -231,8 +228,33 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
             }
         }
     } else {
+        // ------------------------------ Q ------------------------------
+        // rows into K-major swizzled tiles (zeros past D and past the last row), all copies in flight at once
+        if (n > 0) {
+            constexpr int kUnits = DP / 8, kStep = 128 / kUnits;  // rows of a pass of the 128 threads
+            const int c = threadIdx.x % kUnits, r0 = threadIdx.x / kUnits;
+            const uint16_t *base = p.q.ptr + b * p.q.sb + static_cast<long long>(hk) * p.G * p.q.sh + 8 * c;
+            // row -> (query, head of the group), stepped without a division
+            const int dt = kStep / p.G, dg = kStep - dt * p.G;
+            int t = (row0 + r0) / p.G, g = row0 + r0 - t * p.G;
+#pragma unroll 8
+            for (int r = r0; r < 128; r += kStep) {
+                const bool in = row0 + r < rows && 8 * c < p.D;
+                cp_async16(sbase + (c >> 3) * kChunk + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                           in ? base + t * p.q.st + g * p.q.sh : p.q.ptr, in ? 16u : 0u);
+                t += dt;
+                g += dg;
+                if (g >= p.G) {
+                    g -= p.G;
+                    ++t;
+                }
+            }
+            cp_async_wait_all();
+            fence_proxy_async_smem();
+            mbar_arrive(bar_q);
+        }
+
         // ------------------------------ softmax, a row a thread ------------------------------
-        const int row = row0 + threadIdx.x;
         const bool warp_on = row0 + warp * 32 < rows;  // some row of this warp exists
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
         const float c = p.scale_log2;
@@ -373,25 +395,36 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
         if (ok && n > 0) ok = mbar_wait(bar_all, 0, abort_flag, p.status, kStatusTimeoutAccum);
         tc_fence_after();
         if (__all_sync(0xffffffffu, ok) && warp_on) {
-            const bool on = row < rows;
-            const int t = row / p.G, h = hk * p.G + row % p.G;
+            // through shared memory (the ring is idle now), so that a warp stores whole rows: a row a thread
+            // would touch 32 lines per instruction
             const float f = l != 0.0f ? 1.0f / l : 0.0f;
+            const size_t row_g = (static_cast<size_t>(b) * p.Hkv + hk) * rows + row0 + warp * 32;
+            const int live = min(32, rows - row0 - warp * 32);
             if (p.splits > 1) {
-                const size_t at = ((static_cast<size_t>(b) * p.Hkv + hk) * rows + row) * p.splits + split;
-                if (on) p.part_ml[at] = make_float2(m, l);
-                for (int e = 0; e < p.D && n > 0; e += 32) {
-                    uint32_t o[32];
-                    tmem_ld_32x32b_x32(lane_base + e, o);
-                    tmem_ld_wait();
-                    float4 *to = reinterpret_cast<float4 *>(p.part_o + at * p.D + e);
+                constexpr int kPitch = DP * 4;
+                uint8_t *st = smem + C::kOffRing + warp * 32 * kPitch;
+                if (lane < live) p.part_ml[(row_g + lane) * p.splits + split] = make_float2(m, l);
+                if (n > 0) {
+                    for (int e = 0; e < p.D; e += 32) {
+                        uint32_t o[32];
+                        tmem_ld_32x32b_x32(lane_base + e, o);
+                        tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (on && e + 4 * j < p.D)
-                            to[j] = make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]),
-                                                __uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 3]));
+                        for (int j = 0; j < 8; ++j)
+                            *reinterpret_cast<uint4 *>(st + lane * kPitch + (((e >> 2) + j) ^ (lane & 7)) * 16) =
+                                make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                    }
+                    __syncwarp();
+                    const int units = p.D >> 2, lanes = units < 32 ? 32 / units : 1;  // rows an instruction
+                    const int r0 = units < 32 ? lane / units : 0, c0 = units < 32 ? lane % units : lane;
+                    for (int r = r0; r < live && r0 < lanes; r += lanes)
+                        for (int c = c0; c < units; c += 32)
+                            *reinterpret_cast<uint4 *>(p.part_o + ((row_g + r) * p.splits + split) * p.D + 4 * c) =
+                                *reinterpret_cast<const uint4 *>(st + r * kPitch + (c ^ (r & 7)) * 16);
                 }
             } else {
-                uint16_t *to = p.out.ptr + b * p.out.sb + t * p.out.st + h * p.out.sh;
+                constexpr int kPitch = DP * 2;
+                uint8_t *st = smem + C::kOffRing + warp * 32 * kPitch;
                 for (int e = 0; e < p.D; e += 32) {
                     uint32_t o[32];
                     tmem_ld_32x32b_x32(lane_base + e, o);
@@ -407,8 +440,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
                         for (int q = 0; q < 4; ++q)
                             w[q] = pack_bf16x2_rn(__uint_as_float(o[8 * j + 2 * q]) * f,
                                                   __uint_as_float(o[8 * j + 2 * q + 1]) * f);
-                        if (on && e + 8 * j < p.D)
-                            *reinterpret_cast<uint4 *>(to + e + 8 * j) = make_uint4(w[0], w[1], w[2], w[3]);
+                        *reinterpret_cast<uint4 *>(st + lane * kPitch + (((e >> 3) + j) ^ (lane & 7)) * 16) =
+                            make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+                __syncwarp();
+                const int units = p.D >> 3, lanes = 32 / units;  // units <= 32
+                const int r0 = lane / units, c = lane % units;
+                uint16_t *to = p.out.ptr + b * p.out.sb + static_cast<long long>(hk) * p.G * p.out.sh + 8 * c;
+                const int dt = lanes / p.G, dg = lanes - dt * p.G;
+                int t = (row0 + warp * 32 + r0) / p.G, g = row0 + warp * 32 + r0 - t * p.G;
+                for (int r = r0; r < live && r0 < lanes; r += lanes) {
+                    *reinterpret_cast<uint4 *>(to + t * p.out.st + g * p.out.sh) =
+                        *reinterpret_cast<const uint4 *>(st + r * kPitch + (c ^ (r & 7)) * 16);
+                    t += dt;
+                    g += dg;
+                    if (g >= p.G) {
+                        g -= p.G;
+                        ++t;
                     }
                 }
             }
