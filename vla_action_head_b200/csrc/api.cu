@@ -490,16 +490,22 @@ bool make_kv_map(CUtensorMap *m, const Heads &x, int D, int H, int S, int B, int
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Parts of the key range for the tile kernel: the number of least modelled time (us).
+// Few rows share a key head: the row kernel; else the tile kernel.
+bool attention_few_rows(const AttnArgs &a) { return static_cast<long long>(a.T) * a.G <= kAttentionRows; }
+
+// Parts of the key range: the number of least modelled time (us).
 int attention_splits(const AttnArgs &a) {
-    const int slots = sm_count_cached() * (a.D <= 128 ? 2 : 1);
-    const long long tiles = (static_cast<long long>(a.T) * a.G + 127) / 128 * a.B * a.Hkv;
-    const int keys = (a.S + 127) / 128;
+    const bool few = attention_few_rows(a);
+    const int slots = sm_count_cached() * (!few && a.D <= 128 ? 2 : 1);
+    const long long tiles = (few ? 1 : (static_cast<long long>(a.T) * a.G + 127) / 128) * a.B * a.Hkv;
+    const int unit = few ? 128 : 128;  // keys of a step of a CTA
+    const int keys = (a.S + unit - 1) / unit;
+    const double each = few ? (a.cached ? 0.8 : 3.0) * a.D / 256.0 : 1.2;
     int best = 1;
     double best_cost = 1e300;
-    for (int s = 1; s <= keys && s <= 64 && tiles * (s - 1) < slots; ++s) {
+    for (int s = 1; s <= keys && s <= slots && tiles * (s - 1) < 2 * slots; ++s) {
         const double waves = std::ceil(static_cast<double>(tiles * s) / slots);
-        const double cost = waves * ((keys + s - 1) / s * 1.2 + 3.0) + (s > 1 ? 3.0 + 0.05 * s : 0.0);
+        const double cost = waves * ((keys + s - 1) / s * each + 3.0) + (s > 1 ? 3.0 + 0.05 * s : 0.0);
         if (cost < best_cost) {
             best_cost = cost;
             best = s;
@@ -557,7 +563,7 @@ nvfp4_status attention_args(const nvfp4_attention_args &x, AttnArgs *a, bool *em
     a->k_mul_b = a->k.sb != 0;
     a->v_mul_h = a->v.sh != 0;
     a->v_mul_b = a->v.sb != 0;
-    a->splits = a->cached ? 1 : attention_splits(*a);
+    a->splits = a->cached && !attention_few_rows(*a) ? 1 : attention_splits(*a);
     return NVFP4_OK;
 }
 
@@ -572,7 +578,7 @@ nvfp4_status nvfp4_probe(void) {
     if (probe_norm_kernels() != cudaSuccess || probe_gemm_kernels() != cudaSuccess ||
         probe_gemm_persistent() != cudaSuccess ||
         probe_gemm_grouped() != cudaSuccess || probe_attention() != cudaSuccess ||
-        probe_attention_tiles() != cudaSuccess) {
+        probe_attention_tiles() != cudaSuccess || probe_attention_rows() != cudaSuccess) {
         cudaGetLastError();
         return NVFP4_ERR_UNSUPPORTED_DEVICE;
     }
@@ -1090,7 +1096,10 @@ nvfp4_status nvfp4_attention(const nvfp4_attention_args *x, nvfp4_stream_t strea
     if (st != NVFP4_OK) return st;
     if ((a.status = status_word()) == nullptr) return NVFP4_ERR_CUDA;
     cudaError_t e;
-    if (a.cached || a.S == 0) {
+    if (attention_few_rows(a)) {
+        e = launch_attention_rows(a, stream);
+        if (e == cudaSuccess && a.splits > 1) e = launch_attention_join(a, stream);
+    } else if (a.cached || a.S == 0) {
         e = launch_attention(a, stream);
     } else {
         CUtensorMap mk, mv;

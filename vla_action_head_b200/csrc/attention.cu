@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnArgs p) {
 }
 
 // Joins the parts of a split key range: with M the largest reference of the parts that have a sum,
-// out = sum_s 2^(c (m_s - M)) O_s / sum_s 2^(c (m_s - M)) l_s, in the order of s.  A warp a row.
+// out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s (references in units of log2), in the order of s.  A warp a row.
 __global__ void __launch_bounds__(kThreads) attention_join_kernel(const AttnArgs p) {
     pdl_launch_dependents();
     pdl_wait();
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kThreads) attention_join_kernel(const AttnArgs
     for (int s = 0; s < p.splits; ++s) {
         const float2 x = __ldcg(ml + s);
         if (x.y == 0.0f) continue;
-        const float f = exp2f((x.x - M) * p.scale_log2);
+        const float f = exp2f(x.x - M);
         l = fmaf(f, x.y, l);
         if (e0 < p.D) {
             const float4 a = __ldcg(reinterpret_cast<const float4 *>(po + static_cast<size_t>(s) * p.D + e0));

@@ -62,7 +62,7 @@ struct AttnArgs {
     int k_mul_h, k_mul_b, v_mul_h, v_mul_b;  // 0: that dimension is broadcast, its tensor-map size 1
     int splits;      // parts of the key range; > 1: joined from part_o and part_ml
     float *part_o;   // [rows of all heads, splits, D]: unnormalized sums
-    float2 *part_ml; // [rows of all heads, splits]: reference, sum of weights
+    float2 *part_ml; // [rows of all heads, splits]: reference in units of log2, sum of weights
     uint32_t *status;
 };
 cudaError_t launch_attention(const AttnArgs &a, cudaStream_t s);
@@ -74,5 +74,10 @@ cudaError_t probe_attention();
 int attention_v_box_rows(int D);
 cudaError_t launch_attention_tiles(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a, cudaStream_t s);
 cudaError_t probe_attention_tiles();
+
+// Up to kAttentionRows (query, head) pairs per key head, keys streamed through registers.
+constexpr int kAttentionRows = 8;
+cudaError_t launch_attention_rows(const AttnArgs &a, cudaStream_t s);
+cudaError_t probe_attention_rows();
 
 }  // namespace nvfp4

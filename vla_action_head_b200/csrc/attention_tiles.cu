@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
     pdl_launch_dependents();
     pdl_wait();  // q, k, v and kv_len may come from the previous kernel
     int len = p.S;
-    if (p.kv_len != nullptr) len = min(max(__ldg(p.kv_len + b), 0), p.S);
+    if (p.kv_len != nullptr) len = min(max(__ldcg(p.kv_len + b), 0), p.S);
     const int all_tiles = (len + 127) >> 7, per = (all_tiles + p.splits - 1) / p.splits;
     const int tile0 = split * per, n = max(0, min(per, all_tiles - tile0));
     const int kc = (p.D + 63) >> 6;  // 64-element blocks of a head
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
                 for (int w = 0; w < 4; ++w) {
                     const int j = j0 + 32 * w + lane;
                     bool in = j < len;
-                    if (in && p.mask != nullptr) in = __ldg(p.mask + b * p.mask_stride + j) != 0;
+                    if (in && p.mask != nullptr) in = __ldcg(p.mask + b * p.mask_stride + j) != 0;
                     keep[w] = __ballot_sync(0xffffffffu, in);
                 }
             }
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
             if (p.splits > 1) {
                 constexpr int kPitch = DP * 4;
                 uint8_t *st = smem + C::kOffRing + warp * 32 * kPitch;
-                if (lane < live) p.part_ml[(row_g + lane) * p.splits + split] = make_float2(m, l);
+                if (lane < live) p.part_ml[(row_g + lane) * p.splits + split] = make_float2(m * c, l);
                 if (n > 0) {
                     for (int e = 0; e < p.D; e += 32) {
                         uint32_t o[32];
