@@ -465,7 +465,8 @@ typedef struct {
     const int32_t *positions;       /* [B, T] table rows; NULL: start[b] + t */
     const int32_t *start;           /* [B] cache row of each sequence's token 0; NULL: 0 */
     const int32_t *count;           /* [B] tokens of each sequence in this call; NULL: T */
-    const nvfp4_kv_cache *cache;    /* host pointer; NULL: k goes to k_out */
+    nvfp4_kv_cache cache;           /* with cached = 1 */
+    int64_t cached;                 /* 0: k goes to k_out; 1: k and v go to the cache */
 } nvfp4_qk_args;
 
 /* For each token t < count[b] and head:
@@ -489,7 +490,7 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache *cache, const int32_t *start, in
 
 typedef struct {
     int B, T;       /* sequences, queries of each */
-    int S;          /* key rows: of k and v, or <= cache->length */
+    int S;          /* key rows: of k and v, or <= cache.length */
     int Hq, Hkv;    /* Hq % Hkv == 0: query head h reads key head h / (Hq / Hkv) */
     int D;          /* head size: D % 8 == 0, 8 <= D <= 256 (a cache: D % 16 == 0) */
     float scale;    /* > 0, finite */
@@ -497,9 +498,8 @@ typedef struct {
     const int32_t *kv_len;       /* [B] keys of each sequence, clamped to [0, S]; NULL: S */
     const uint8_t *key_mask;     /* [B, S], 0: the key is left out; NULL: none is */
     int64_t mask_stride;         /* elements between the mask's sequences */
-    const nvfp4_kv_cache *cache; /* host pointer; NULL: k and v */
-    void *workspace;
-    size_t ws_bytes;
+    nvfp4_kv_cache cache;        /* with cached = 1 */
+    int64_t cached;              /* 0: keys and values are k and v; 1: the cache's */
 } nvfp4_attention_args;
 
 /* out[b, t, h] = sum_j p_j v_j,  p = softmax_j(scale * q[b, t, h] . k_j) over the keys
@@ -509,7 +509,8 @@ typedef struct {
  * values) or fp16 (cache) for their product with the values; out is rounded once to bf16.
  * B, T, S = 0: nothing is read (S = 0: zeros are written).  Results do not depend on timing.
  * workspace: nvfp4_attention_workspace_bytes, used by one call at a time, any contents. */
-nvfp4_status nvfp4_attention(const nvfp4_attention_args *a, nvfp4_stream_t stream);
+nvfp4_status nvfp4_attention(const nvfp4_attention_args *a, void *workspace, size_t ws_bytes,
+                             nvfp4_stream_t stream);
 size_t nvfp4_attention_workspace_bytes(const nvfp4_attention_args *a);
 
 #ifdef __cplusplus

@@ -36,8 +36,7 @@ def qk(**kw):
 
 
 def at(**kw):
-    d = dict(B=2, T=4, S=50, Hq=8, Hkv=1, D=256, scale=0.1, q=heads(), k=heads(), v=heads(), out=heads(),
-             workspace=0x100000, ws_bytes=1 << 40)
+    d = dict(B=2, T=4, S=50, Hq=8, Hkv=1, D=256, scale=0.1, q=heads(), k=heads(), v=heads(), out=heads())
     d.update(kw)
     return nvfp4._AttentionArgs(**d)
 
@@ -59,8 +58,9 @@ def test_qk_refusals(L):
     # nothing to do: no pointer is read
     assert f(B=0, q=heads(None), k=heads(None)) == 0 and f(Hq=0, Hkv=0) == 0
     assert f() in NO_DEVICE
+    assert f(cached=2) == INVALID
     # with a cache
-    g = lambda c, **kw: f(cache=C.pointer(c), **kw)  # noqa: E731
+    g = lambda c, **kw: f(cache=c, cached=1, **kw)  # noqa: E731
     assert g(cache(), v=heads(None)) == INVALID
     assert g(cache(), Hkv=0) == INVALID
     assert g(cache(), k_out=heads(None)) in NO_DEVICE
@@ -83,8 +83,9 @@ def test_kv_read_refusals(L):
 
 
 def test_attention_refusals(L):
-    f = lambda **kw: L.nvfp4_attention(C.byref(at(**kw)), None)  # noqa: E731
-    assert L.nvfp4_attention(None, None) == INVALID
+    f = lambda **kw: L.nvfp4_attention(C.byref(at(**kw)), 0x100000, 1 << 40, None)  # noqa: E731
+    assert L.nvfp4_attention(None, None, 0, None) == INVALID
+    assert f(cached=2) == INVALID
     for kw in (dict(B=-1), dict(T=-1), dict(S=-1), dict(Hq=0), dict(Hkv=0), dict(D=0), dict(scale=0.0),
                dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(q=heads(None)),
                dict(k=heads(None)), dict(v=heads(None)), dict(out=heads(None)), dict(k=heads(st=-8)),
@@ -96,7 +97,7 @@ def test_attention_refusals(L):
         assert f(**kw) == MISALIGNED, kw
     assert f(B=0) == 0 and f(T=0) == 0
     assert f() in NO_DEVICE
-    g = lambda c, **kw: f(cache=C.pointer(c), k=heads(None), v=heads(None), **kw)  # noqa: E731
+    g = lambda c, **kw: f(cache=c, cached=1, k=heads(None), v=heads(None), **kw)  # noqa: E731
     assert g(cache()) in NO_DEVICE
     assert g(cache(), S=51) == INVALID
     assert g(cache(H=2)) == INVALID and g(cache(B=1)) == INVALID
@@ -109,9 +110,11 @@ def test_workspace_query(L):
     need = L.nvfp4_attention_workspace_bytes(C.byref(big))
     assert L.nvfp4_attention_workspace_bytes(C.byref(at(T=1, S=1))) == 0
     assert L.nvfp4_attention_workspace_bytes(C.byref(at(D=7))) == 0
-    if need:
-        big.ws_bytes = need - 1
-        assert L.nvfp4_attention(C.byref(big), None) in (WORKSPACE,) + NO_DEVICE
+    assert need > 0
+    assert L.nvfp4_attention(C.byref(big), 0x100000, need - 1, None) == WORKSPACE
+    assert L.nvfp4_attention(C.byref(big), None, need, None) == WORKSPACE
+    assert L.nvfp4_attention(C.byref(big), 0x100008, need, None) == MISALIGNED
+    assert L.nvfp4_attention(C.byref(big), 0x100000, need, None) in NO_DEVICE
 
 
 def test_binding_refusals():

@@ -529,14 +529,15 @@ nvfp4_status attention_args(const nvfp4_attention_args &x, AttnArgs *a, bool *em
     *a = AttnArgs{};
     *empty = x.B == 0 || x.T == 0;
     nvfp4_status st = NVFP4_OK;
-    if (x.cache != nullptr) {
-        st = check_cache(*x.cache, x.B, x.Hkv, x.D, &a->cache);
-        if (st == NVFP4_OK && x.S > x.cache->length) st = NVFP4_ERR_INVALID_ARG;
+    if (x.cached != 0 && x.cached != 1) return NVFP4_ERR_INVALID_ARG;
+    if (x.cached) {
+        st = check_cache(x.cache, x.B, x.Hkv, x.D, &a->cache);
+        if (st == NVFP4_OK && x.S > x.cache.length) st = NVFP4_ERR_INVALID_ARG;
     }
     if (st != NVFP4_OK || *empty) return st;
     st = check_heads(x.q, x.B, x.T, x.Hq, x.D, false, &a->q);
     if (st == NVFP4_OK) st = check_heads(x.out, x.B, x.T, x.Hq, x.D, true, &a->out);
-    if (st == NVFP4_OK && x.cache == nullptr && x.S > 0) {
+    if (st == NVFP4_OK && !x.cached && x.S > 0) {
         st = check_heads(x.k, x.B, x.S, x.Hkv, x.D, false, &a->k);
         if (st == NVFP4_OK) st = check_heads(x.v, x.B, x.S, x.Hkv, x.D, false, &a->v);
         // keys that share one row are not a cache of keys
@@ -553,7 +554,7 @@ nvfp4_status attention_args(const nvfp4_attention_args &x, AttnArgs *a, bool *em
     a->Hkv = x.Hkv;
     a->D = x.D;
     a->G = x.Hq / x.Hkv;
-    a->cached = x.cache != nullptr ? 1 : 0;
+    a->cached = static_cast<int>(x.cached);
     a->scale_log2 = static_cast<float>(static_cast<double>(x.scale) * 1.4426950408889634 *
                                        (a->cached ? static_cast<double>(a->cache.k.g) : 1.0));
     a->kv_len = x.kv_len;
@@ -995,11 +996,12 @@ nvfp4_status nvfp4_qk_norm_rope(const nvfp4_qk_args *x, nvfp4_stream_t stream) {
     if (x->norm && (!(x->eps >= 0.0f) || !std::isfinite(x->eps))) return NVFP4_ERR_INVALID_ARG;
     if (!x->norm && (x->q_gamma != nullptr || x->k_gamma != nullptr)) return NVFP4_ERR_INVALID_ARG;
     QkArgs a = {};
-    const bool cached = x->cache != nullptr;
+    if (x->cached != 0 && x->cached != 1) return NVFP4_ERR_INVALID_ARG;
+    const bool cached = x->cached == 1;
     nvfp4_status st = NVFP4_OK;
     if (cached) {
         if (x->Hkv == 0) return NVFP4_ERR_INVALID_ARG;
-        st = check_cache(*x->cache, x->B, x->Hkv, x->D, &a.cache);
+        st = check_cache(x->cache, x->B, x->Hkv, x->D, &a.cache);
         if (st != NVFP4_OK) return st;
     }
     if (x->B == 0 || x->T == 0 || (x->Hq == 0 && x->Hkv == 0)) return NVFP4_OK;
@@ -1079,7 +1081,7 @@ size_t nvfp4_attention_workspace_bytes(const nvfp4_attention_args *x) {
     return attention_workspace(a);
 }
 
-nvfp4_status nvfp4_attention(const nvfp4_attention_args *x, nvfp4_stream_t stream) {
+nvfp4_status nvfp4_attention(const nvfp4_attention_args *x, void *workspace, size_t ws_bytes, nvfp4_stream_t stream) {
     if (x == nullptr) return NVFP4_ERR_INVALID_ARG;
     AttnArgs a;
     bool empty = false;
@@ -1087,9 +1089,9 @@ nvfp4_status nvfp4_attention(const nvfp4_attention_args *x, nvfp4_stream_t strea
     if (st != NVFP4_OK || empty) return st;
     const size_t need = attention_workspace(a);
     if (need > 0) {
-        if (x->workspace == nullptr || x->ws_bytes < need) return NVFP4_ERR_WORKSPACE;
-        if (!aligned16(x->workspace)) return NVFP4_ERR_MISALIGNED;
-        a.part_o = static_cast<float *>(x->workspace);
+        if (workspace == nullptr || ws_bytes < need) return NVFP4_ERR_WORKSPACE;
+        if (!aligned16(workspace)) return NVFP4_ERR_MISALIGNED;
+        a.part_o = static_cast<float *>(workspace);
         a.part_ml = reinterpret_cast<float2 *>(a.part_o + static_cast<size_t>(a.B) * a.T * a.Hq * a.splits * a.D);
     }
     st = check_device();

@@ -5,7 +5,7 @@
 //
 // The work is the stream of keys and values, so the matrix instruction is the one that takes its
 // operands from registers (m16n8k16): 16 keys (or 16 elements of V) are its rows, the 8 query
-// rows its columns.  Nothing but the result passes through shared memory.  A contraction may take
+// rows its columns.  A contraction may take
 // its elements in any order as long as both sides do, so every thread takes runs of adjacent
 // elements: of a key the quarter of its lane % 4 (k of S^T), of a value row the eighth of its
 // lane / 4 (the rows of O^T), which makes 16-byte loads of plain rows.  The weights turn from S^T's
@@ -14,8 +14,13 @@
 // Cache: codes become fp16 (exact: 2-bit significand times 4-bit scale; the weights are then fp16
 // too, closer than bf16).  Query rows are scaled by a power of two into fp16's range, which changes no bit of them.
 //
-// 8 warps of a CTA take every eighth step of 16 keys and are joined through shared memory; one
-// CTA takes a range of keys, and the ranges of a long sequence are joined by attention_join_kernel.
+// The loads are asynchronous copies, kStages - 1 steps of 16 keys ahead, and each thread copies just
+// what it will read itself into a place of its own: no barrier in the loop, conflict-free shared
+// memory, and 100 KB and more on their way per SM (loads into registers left one step in flight:
+// 71 us instead of XX for 8 sequences of 32701 cached keys, 256-wide heads).
+//
+// The warps of a CTA take turns at the steps and are joined through shared memory; one CTA takes a
+// range of keys, and the ranges of a long sequence are joined by attention_join_kernel.
 // The reference m of a row is replaced only when a score outgrows it by 2^8, found by one vote a
 // step, so the steps carry no reductions; l stays per thread until the end.
 #include <cuda_fp16.h>
@@ -31,7 +36,6 @@ namespace nvfp4 {
 
 namespace {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kRows = 8;
 constexpr float kLazy = 8.0f;
 
@@ -77,50 +81,89 @@ __device__ __forceinline__ uint32_t scale_f16x2(uint32_t byte) {
     return r;
 }
 
-// A run of N elements of a row, N a multiple of 16 (or 8: half a block), as N / 2 16-bit pairs;
-// zeros for rows that are left out and elements past D.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, bool on) {
+    const uint32_t n = on ? BYTES : 0u;  // 0: zeros
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n)
+                     : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {  // all but the newest N groups have landed
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds4(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+
+// A run of N adjacent elements of a row (from e0) as it passes through this thread's places of a
+// stage: kBytes per lane, the lanes' pieces of a copy side by side.
+//   copy: global -> shared, zeros for rows that do not exist and elements past D
+//   load: shared -> registers;  keep = 0 makes the run zero whatever its bytes are
+//   pairs(i): elements 8i .. 8i + 7 as four 16-bit pairs
 template <int N, bool FULL>
-struct CodeRun {  // NVFP4
+struct CodeRun {  // NVFP4; FULL: D fills the kernel's width, so rows are aligned as runs are
     static constexpr int kWords = N / 8, kScales = N >= 16 ? N / 16 : 1;
+    static constexpr int kPiece = N / 2 < 8 ? 4 : FULL && N / 2 >= 16 ? 16 : 8, kPieces = N / 2 / kPiece;
+    static constexpr int kScaleWords = FULL || kScales == 1 ? 1 : 2;  // a run's bytes may cross a word
+    static constexpr int kBytes = N / 2 + 4 * kScaleWords;
     uint32_t w[kWords], s[kScales];
-    __device__ __forceinline__ void load(const uint8_t *codes, const uint8_t *sf, int e0, int D, bool on) {
-        // left out: a zero scale, as 0 times any code is 0
+
+    __device__ __forceinline__ static void copy(uint32_t dst, int lane, const CachePlane &c, size_t row, int e0, int D,
+                                                bool on) {
+        const uint8_t *codes = c.codes + row * (D >> 1) + (e0 >> 1);
 #pragma unroll
-        for (int i = 0; i < kWords; ++i) w[i] = 0u;
-#pragma unroll
-        for (int i = 0; i < kScales; ++i) s[i] = 0u;
-        if constexpr (FULL && N % 32 == 0) {
-            if (on) {
-#pragma unroll
-                for (int i = 0; i < kWords / 4; ++i) {
-                    const uint4 u = __ldcg(reinterpret_cast<const uint4 *>(codes + (e0 >> 1)) + i);
-                    w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
-                }
-                if constexpr (kScales == 4) {
-                    const uint32_t u = __ldcg(reinterpret_cast<const uint32_t *>(sf + (e0 >> 4)));
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) s[i] = (u >> (8 * i)) & 255u;
-                } else {
-                    const uint32_t u = __ldcg(reinterpret_cast<const uint16_t *>(sf + (e0 >> 4)));
-                    s[0] = u & 255u;
-                    s[1] = u >> 8;
-                }
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < kScales; ++i)
-                if (on && e0 + 16 * i < D) {
-                    if constexpr (N >= 16) {
-                        const uint2 u = __ldcg(reinterpret_cast<const uint2 *>(codes + (e0 >> 1)) + i);
-                        w[2 * i] = u.x, w[2 * i + 1] = u.y;
-                    } else {
-                        w[0] = __ldcg(reinterpret_cast<const uint32_t *>(codes + (e0 >> 1)));
-                    }
-                    s[i] = __ldcg(sf + (e0 >> 4) + i);
-                }
+        for (int i = 0; i < kPieces; ++i) {
+            const bool in = on && e0 + 2 * kPiece * i < D;
+            copy_async<kPiece>(dst + i * 32 * kPiece + lane * kPiece, in ? codes + i * kPiece : c.codes, in);
+        }
+        // whole words that hold the scale bytes (the plane's size is a multiple of 16 bytes)
+        const size_t at = row * (D >> 4) + (e0 >> 4);
+        const int last = static_cast<int>(at & 3) + kScales - 1;
+        const bool in = on && e0 < D;
+        copy_async<4>(dst + 16 * N + lane * 4, in ? c.sf + (at & ~size_t(3)) : c.sf, in);
+        if constexpr (kScaleWords == 2) {
+            const bool two = in && last >= 4 && e0 + 16 * (4 - static_cast<int>(at & 3)) < D;
+            copy_async<4>(dst + 16 * N + 128 + lane * 4, two ? c.sf + (at & ~size_t(3)) + 4 : c.sf, two);
         }
     }
-    // elements 8i .. 8i + 7 as four pairs
+    __device__ __forceinline__ void load(uint32_t src, int lane, size_t row, int e0, int D, bool keep) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const uint32_t a = src + i * 32 * kPiece + lane * kPiece;
+            if constexpr (kPiece == 16) {
+                const uint4 u = lds16(a);
+                w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+            } else if constexpr (kPiece == 8) {
+                const uint2 u = lds8(a);
+                w[2 * i] = u.x, w[2 * i + 1] = u.y;
+            } else {
+                w[0] = lds4(a);
+            }
+        }
+        const uint32_t off = 8u * static_cast<uint32_t>((FULL ? (e0 >> 4) : static_cast<int>(row * (D >> 4) + (e0 >> 4))) & 3);
+        uint32_t x = lds4(src + 16 * N + lane * 4);
+        if constexpr (kScaleWords == 2) x = __funnelshift_r(x, lds4(src + 16 * N + 128 + lane * 4), off);
+        else x >>= off;
+        if (!keep) x = 0u;
+#pragma unroll
+        for (int i = 0; i < kScales; ++i) s[i] = (FULL || e0 + 16 * i < D) ? (x >> (8 * i)) & 255u : 0u;
+    }
     __device__ __forceinline__ void pairs(int i, uint32_t (&h)[4]) const {
         decode_e2m1x8_f16(w[i], h);
         const uint32_t sc = scale_f16x2(s[i / 2]);
@@ -130,8 +173,23 @@ struct CodeRun {  // NVFP4
 };
 template <int N>
 struct WideRun {  // bf16
+    static constexpr int kBytes = 2 * N;
     uint4 u[N / 8];
-    __device__ __forceinline__ void load(const uint16_t *row, int e0, int D, bool on) {
+    __device__ __forceinline__ static void copy(uint32_t dst, int lane, const uint16_t *row, int e0, int D, bool on) {
+#pragma unroll
+        for (int i = 0; i < N / 8; ++i) {
+            const bool in = on && e0 + 8 * i < D;
+            copy_async<16>(dst + i * 512 + lane * 16, in ? row + e0 + 8 * i : row, in);
+        }
+    }
+    __device__ __forceinline__ void load(uint32_t src, int lane, size_t, int, int, bool keep) {
+#pragma unroll
+        for (int i = 0; i < N / 8; ++i) {
+            u[i] = lds16(src + i * 512 + lane * 16);
+            if (!keep) u[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
+    __device__ __forceinline__ void load_global(const uint16_t *row, int e0, int D, bool on) {
 #pragma unroll
         for (int i = 0; i < N / 8; ++i) {
             u[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -152,12 +210,25 @@ struct RunOf<N, FULL, false> {
 };
 
 template <int DP, bool FULL, bool CACHED>
-__global__ void __launch_bounds__(kThreads, 1) attention_rows_kernel(const AttnArgs p) {
+struct Cfg {
+    using KRun = typename RunOf<DP / 4, FULL, CACHED>::type;  // of 2 keys
+    using VRun = typename RunOf<DP / 8, FULL, CACHED>::type;  // of 4 keys
+    static constexpr int kKBytes = 32 * KRun::kBytes, kVBytes = 32 * VRun::kBytes;
+    static constexpr int kStage = 2 * kKBytes + 4 * kVBytes;  // of a warp: 16 KB (bf16) or 5 KB at DP = 256
+    static constexpr int kWarps = !CACHED && DP == 256 ? 4 : 8, kThreads = 32 * kWarps;
+    static constexpr int kStages = !CACHED && DP >= 128 ? 3 : 4;
+    static constexpr int kRing = kWarps * kStages * kStage, kJoin = kWarps * kRows * DP * 4;
+    static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
+    static_assert(kSmem + 1024 <= 232448, "shared memory");
+};
+
+template <int DP, bool FULL, bool CACHED>
+__global__ void __launch_bounds__(Cfg<DP, FULL, CACHED>::kThreads, 1) attention_rows_kernel(const AttnArgs p) {
+    using C = Cfg<DP, FULL, CACHED>;
+    constexpr int kWarps = C::kWarps, kThreads = C::kThreads;
     constexpr int kKRun = DP / 4, kVRun = DP / 8;  // adjacent elements of a thread
     constexpr int kTiles = DP / 16;                // k steps of S^T, row tiles of O^T
-    using KRun = typename RunOf<kKRun, FULL, CACHED>::type;
-    using VRun = typename RunOf<kVRun, FULL, CACHED>::type;
-    extern __shared__ float smem_o[];  // [kWarps][kRows][DP]
+    extern __shared__ __align__(16) float smem_o[];  // the warps' stages, then [kWarps][kRows][DP]
     __shared__ float sm_m[kWarps][kRows], sm_l[kWarps][kRows];
     pdl_launch_dependents();
     pdl_wait();
@@ -169,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_rows_kernel(const AttnA
     const int rows = p.T * p.G;  // <= kRows
     int len = p.S;
     if (p.kv_len != nullptr) len = min(max(__ldcg(p.kv_len + b), 0), p.S);
-    // whole steps of 16 keys to the splits, every eighth step of a split to a warp
+    // whole steps of 16 keys to the splits, in turn to the warps
     const int steps = (len + 15) >> 4, per = (steps + p.splits - 1) / p.splits;
     const int step0 = split * per, step1 = min(steps, step0 + per);
 
@@ -180,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_rows_kernel(const AttnA
         const bool on = g < rows;
         const int tq = on ? g / p.G : 0, hq = hk * p.G + (on ? g - tq * p.G : 0);
         WideRun<kKRun> r;
-        r.load(p.q.ptr + b * p.q.sb + tq * p.q.st + hq * p.q.sh, t * kKRun, p.D, on);
+        r.load_global(p.q.ptr + b * p.q.sb + tq * p.q.st + hq * p.q.sh, t * kKRun, p.D, on);
         if constexpr (CACHED) {
             float top = 0.0f;
 #pragma unroll
@@ -223,32 +294,56 @@ __global__ void __launch_bounds__(kThreads, 1) attention_rows_kernel(const AttnA
         __syncwarp();
     }
 
-    float o[kTiles][4] = {};
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};  // rows 2t, 2t + 1; m in units of log2
     const uint8_t *mask = p.mask != nullptr ? p.mask + b * p.mask_stride : nullptr;
     const size_t plane = (static_cast<size_t>(b) * p.Hkv + hk) * p.cache.C;
     const uint16_t *kbase = p.k.ptr + b * p.k.sb + hk * p.k.sh, *vbase = p.v.ptr + b * p.v.sb + hk * p.v.sh;
+    const uint32_t ring = smem_u32(smem_o) + warp * C::kStages * C::kStage;
+    // a step's keys: g, g + 8 for the scores; 2t, 2t + 1, 2t + 8, 2t + 9 for the values
+    auto copy_step = [&](int st, int slot) {
+        const uint32_t at = ring + slot * C::kStage;
+        if (st < step1) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int j = 16 * st + g + 8 * i;
+                if constexpr (CACHED) C::KRun::copy(at + i * C::kKBytes, lane, p.cache.k, plane + j, t * kKRun, p.D, j < len);
+                else C::KRun::copy(at + i * C::kKBytes, lane, j < len ? kbase + j * p.k.st : kbase, t * kKRun, p.D, j < len);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int j = 16 * st + 2 * t + (i & 1) + 8 * (i >> 1);
+                const uint32_t to = at + 2 * C::kKBytes + i * C::kVBytes;
+                if constexpr (CACHED) C::VRun::copy(to, lane, p.cache.v, plane + j, g * kVRun, p.D, j < len);
+                else C::VRun::copy(to, lane, j < len ? vbase + j * p.v.st : vbase, g * kVRun, p.D, j < len);
+            }
+        }
+        copy_commit();
+    };
+    // lane's key of a step, 1 if it is attended to; asked for one step ahead
+    auto key_on = [&](int st) -> uint32_t {
+        const int j = 16 * st + (lane & 15);
+        if (st >= step1 || j >= len) return 0u;
+        return mask == nullptr ? 1u : __ldcg(mask + j) != 0 ? 1u : 0u;
+    };
+
+    float o[kTiles][4] = {};
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};  // rows 2t, 2t + 1; m in units of log2
+#pragma unroll
+    for (int i = 0; i < C::kStages - 1; ++i) copy_step(step0 + warp + i * kWarps, i);
+    uint32_t key = key_on(step0 + warp);
+    int slot = 0;
     for (int st = step0 + warp; st < step1; st += kWarps) {
-        const int j0 = st << 4;
-        // keys g, g + 8 for the scores; 2t, 2t + 1, 2t + 8, 2t + 9 for the values
-        const int jk[2] = {j0 + g, j0 + g + 8}, jv[4] = {j0 + 2 * t, j0 + 2 * t + 1, j0 + 2 * t + 8, j0 + 2 * t + 9};
-        bool ok[2], vk[4];
+        copy_wait<C::kStages - 2>();
+        copy_step(st + (C::kStages - 1) * kWarps, slot == 0 ? C::kStages - 1 : slot - 1);
+        const uint32_t keys = __ballot_sync(0xffffffffu, key != 0u);
+        key = key_on(st + kWarps);
+        const uint32_t at = ring + slot * C::kStage;
+        slot = slot + 1 == C::kStages ? 0 : slot + 1;
+        const bool ok[2] = {((keys >> g) & 1u) != 0u, ((keys >> (g + 8)) & 1u) != 0u};
+        typename C::KRun kr[2];
+        typename C::VRun vr[4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) ok[i] = jk[i] < len && (mask == nullptr || __ldcg(mask + jk[i]) != 0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) vk[i] = jv[i] < len && (mask == nullptr || __ldcg(mask + jv[i]) != 0);
-        KRun kr[2];
-        VRun vr[4];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if constexpr (CACHED) kr[i].load(p.cache.k.codes + (plane + jk[i]) * (p.D >> 1), p.cache.k.sf + (plane + jk[i]) * (p.D >> 4), t * kKRun, p.D, ok[i]);
-            else kr[i].load(kbase + jk[i] * p.k.st, t * kKRun, p.D, ok[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (CACHED) vr[i].load(p.cache.v.codes + (plane + jv[i]) * (p.D >> 1), p.cache.v.sf + (plane + jv[i]) * (p.D >> 4), g * kVRun, p.D, vk[i]);
-            else vr[i].load(vbase + jv[i] * p.v.st, g * kVRun, p.D, vk[i]);
-        }
+        for (int i = 0; i < 2; ++i)
+            kr[i].load(at + i * C::kKBytes, lane, plane + 16 * st + g + 8 * i, t * kKRun, p.D, true);
         float s[4] = {};
 #pragma unroll
         for (int i = 0; i < kKRun / 8; ++i) {
@@ -289,6 +384,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_rows_kernel(const AttnA
             w[i] = ex2(x[i] - (m[i & 1] == -INFINITY ? 0.0f : m[i & 1]));
             l[i & 1] += w[i];
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int j = 2 * t + (i & 1) + 8 * (i >> 1);
+            vr[i].load(at + 2 * C::kKBytes + i * C::kVBytes, lane, plane + 16 * st + j, g * kVRun, p.D,
+                       mask == nullptr || ((keys >> j) & 1u) != 0u);
+        }
         uint32_t pb[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -307,7 +408,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_rows_kernel(const AttnA
         }
     }
 
-    // ---- join the warps ----
+    // ---- join the warps (in the place of the stages) ----
+    copy_wait<0>();
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
 #pragma unroll
@@ -322,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_rows_kernel(const AttnA
                 make_float2(o[j][i], o[j][2 + i]);
     }
     __syncthreads();
-    constexpr int kPer = kRows * DP / kThreads;  // 2, 4 or 8 adjacent elements a thread
+    constexpr int kPer = kRows * DP / kThreads;  // 2, 4, 8 or 16 adjacent elements a thread
     const int r = threadIdx.x * kPer / DP, e0 = threadIdx.x * kPer % DP;
     float M = -INFINITY;
 #pragma unroll
@@ -337,13 +440,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_rows_kernel(const AttnA
 #pragma unroll
         for (int e = 0; e < kPer; ++e) acc[e] = fmaf(f, smem_o[(w * kRows + r) * DP + e0 + e], acc[e]);
     }
-    if (r >= rows || e0 >= p.D) return;  // D % 8 == 0: a thread's elements are all in or out
+    if (r >= rows) return;
     if (p.splits > 1) {
         const size_t at = ((static_cast<size_t>(b) * p.Hkv + hk) * rows + r) * p.splits + split;
         if (e0 == 0) p.part_ml[at] = make_float2(M, sum);
         if (sum != 0.0f) {
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) p.part_o[at * p.D + e0 + e] = acc[e];
+            for (int e = 0; e < kPer; ++e)
+                if (e0 + e < p.D) p.part_o[at * p.D + e0 + e] = acc[e];
         }
     } else {
         const float f = sum != 0.0f ? (CACHED ? p.cache.v.g : 1.0f) / sum : 0.0f;
@@ -351,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_rows_kernel(const AttnA
         uint16_t *to = p.out.ptr + b * p.out.sb + tq * p.out.st + hq * p.out.sh + e0;
 #pragma unroll
         for (int e = 0; e < kPer; e += 2)
-            *reinterpret_cast<uint32_t *>(to + e) = pack_bf16x2_rn(acc[e] * f, acc[e + 1] * f);
+            if (e0 + e < p.D) *reinterpret_cast<uint32_t *>(to + e) = pack_bf16x2_rn(acc[e] * f, acc[e + 1] * f);
     }
 }
 
@@ -359,15 +463,15 @@ template <int DP, bool FULL, bool CACHED>
 cudaError_t launch_rows(const AttnArgs &a, cudaStream_t s) {
     static std::atomic<bool> attr_set[kMaxDevices];
     auto *kernel = attention_rows_kernel<DP, FULL, CACHED>;
-    constexpr int kSmem = kWarps * kRows * DP * 4;
-    cudaError_t e = set_smem_limit_once(reinterpret_cast<const void *>(kernel), kSmem, attr_set);
+    using C = Cfg<DP, FULL, CACHED>;
+    cudaError_t e = set_smem_limit_once(reinterpret_cast<const void *>(kernel), C::kSmem, attr_set);
     if (e != cudaSuccess) return e;
     const long long ctas = static_cast<long long>(a.B) * a.Hkv * a.splits;
     if (ctas > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmem;
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -11,6 +11,7 @@ Raw entry points keep their C names (`nvfp4_quantize_norm`, `nvfp4_quantize_weig
 import ctypes as C
 import os
 import re
+import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -71,14 +72,31 @@ class _QkArgs(C.Structure):
                 ("pairs", C.c_int), ("norm", C.c_int), ("eps", C.c_float), ("q", _Heads), ("k", _Heads),
                 ("v", _Heads), ("q_out", _Heads), ("k_out", _Heads), ("q_gamma", C.c_void_p),
                 ("k_gamma", C.c_void_p), ("table", C.c_void_p), ("table_rows", C.c_int), ("positions", C.c_void_p),
-                ("start", C.c_void_p), ("count", C.c_void_p), ("cache", C.POINTER(_KVCache))]
+                ("start", C.c_void_p), ("count", C.c_void_p), ("cache", _KVCache), ("cached", C.c_int64)]
 
 
 class _AttentionArgs(C.Structure):
     _fields_ = [("B", C.c_int), ("T", C.c_int), ("S", C.c_int), ("Hq", C.c_int), ("Hkv", C.c_int), ("D", C.c_int),
                 ("scale", C.c_float), ("q", _Heads), ("k", _Heads), ("v", _Heads), ("out", _Heads),
                 ("kv_len", C.c_void_p), ("key_mask", C.c_void_p), ("mask_stride", C.c_int64),
-                ("cache", C.POINTER(_KVCache)), ("workspace", C.c_void_p), ("ws_bytes", C.c_size_t)]
+                ("cache", _KVCache), ("cached", C.c_int64)]
+
+
+def _packer(struct_type):
+    """struct.Struct with the layout of a ctypes structure (nested ones in place): one call packs a
+    whole argument structure, at a fraction of the cost of setting ctypes fields."""
+    codes = {C.c_int: "i", C.c_float: "f", C.c_void_p: "P", C.c_int64: "q"}
+
+    def fmt(t):
+        return "".join(codes.get(f) or fmt(f) + "0P" for _, f in t._fields_)
+
+    p = struct.Struct("@" + fmt(struct_type) + "0P")
+    assert p.size == C.sizeof(struct_type)
+    return p
+
+
+_PACK_QK, _PACK_ATTENTION, _PACK_CACHE = _packer(_QkArgs), _packer(_AttentionArgs), _packer(_KVCache)
+_NO_HEADS, _NO_CACHE = (0, 0, 0, 0), (0, 0, 0, 0, 0.0, 0.0, 0, 0, 0, 0, 0)
 
 
 _lib = None
@@ -117,10 +135,11 @@ def lib():
                                                     P]),
             "nvfp4_gemm": (I, [C.POINTER(_Tensor), C.POINTER(_Tensor), I, I, I, I, P, P, I, P, I, P, P,
                                F, P, SZ, P]),
-            "nvfp4_qk_norm_rope": (I, [C.POINTER(_QkArgs), P]),
-            "nvfp4_kv_read": (I, [C.POINTER(_KVCache), P, I, _Heads, _Heads, P]),
-            "nvfp4_attention": (I, [C.POINTER(_AttentionArgs), P]),
-            "nvfp4_attention_workspace_bytes": (SZ, [C.POINTER(_AttentionArgs)]),
+            # argument structures as bytes (packed) or by reference
+            "nvfp4_qk_norm_rope": (I, [P, P]),
+            "nvfp4_kv_read": (I, [P, P, I, _Heads, _Heads, P]),
+            "nvfp4_attention": (I, [P, P, SZ, P]),
+            "nvfp4_attention_workspace_bytes": (SZ, [P]),
             "nvfp4_program_bytes": (SZ, [I]),
             "nvfp4_program_build": (I, [C.POINTER(_Op), I, P, SZ, C.POINTER(_Program)]),
             "nvfp4_program_run": (I, [C.POINTER(_Program), P]),
@@ -152,9 +171,15 @@ def _check(call, st):
 
 
 # ---- torch-facing helpers ---------------------------------------------------------------
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t):
@@ -444,16 +469,21 @@ class KVCache:
     length: Optional[int] = None
 
     def c(self):
+        """The fields of an nvfp4_kv_cache, in order."""
         torch = _torch()
-        B, H, cap, d2 = self.k_codes.shape
-        for n, t, w in (("k_codes", self.k_codes, d2), ("k_sf", self.k_sf, d2 // 8),
-                        ("v_codes", self.v_codes, d2), ("v_sf", self.v_sf, d2 // 8)):
-            if t.dtype != torch.uint8 or tuple(t.shape) != (B, H, cap, w) or not t.is_contiguous():
-                raise ValueError(f"{n} must be a dense uint8 tensor of shape {(B, H, cap, w)}")
-            if t.device != self.k_codes.device:
-                raise ValueError(f"{n} is on {t.device}, k_codes on {self.k_codes.device}")
-        return _KVCache(self.k_codes.data_ptr(), self.k_sf.data_ptr(), self.v_codes.data_ptr(),
-                        self.v_sf.data_ptr(), self.k_scale, self.v_scale, B, H, cap, 2 * d2, self.rows())
+        u8, kc, ks, vc, vs = torch.uint8, self.k_codes, self.k_sf, self.v_codes, self.v_sf
+        shape = kc.shape
+        if len(shape) != 4:
+            raise ValueError(f"k_codes must be [B, H, capacity, D/2], got {tuple(shape)}")
+        B, H, cap, d2 = shape
+        sf, dev = (B, H, cap, d2 // 8), kc.device
+        for n, t, w in (("k_codes", kc, shape), ("k_sf", ks, sf), ("v_codes", vc, shape), ("v_sf", vs, sf)):
+            if t.dtype is not u8 or t.shape != w or not t.is_contiguous():
+                raise ValueError(f"{n} must be a dense uint8 tensor of shape {tuple(w)}")
+            if t.device != dev:
+                raise ValueError(f"{n} is on {t.device}, k_codes on {dev}")
+        return (kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), self.k_scale, self.v_scale, B, H, cap,
+                2 * d2, cap if self.length is None else self.length)
 
     def rows(self):
         return self.k_codes.shape[2] if self.length is None else int(self.length)
@@ -468,43 +498,54 @@ def empty_kv_cache(B, length, H, D, device="cuda", k_scale=1.0, v_scale=1.0) -> 
 
 
 def _tensor(name, t, dtype, shape, device):
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
-    return t
 
 
 def _heads(name, t, shape, device):
-    """A bf16 [B, T, H, D] view, the elements of a head adjacent."""
+    """The fields of an nvfp4_heads for a bf16 [B, T, H, D] view, the elements of a head adjacent."""
     if t is None:
         raise ValueError(f"{name} is missing")
     _tensor(name, t, _torch().bfloat16, shape, device)
-    s = t.stride()
-    if shape[3] > 1 and s[3] != 1:
+    sb, st, sh, sd = t.stride()
+    if sd != 1 and shape[3] > 1:
         raise ValueError(f"{name}: the elements of a head must be adjacent")
-    return _Heads(t.data_ptr(), s[0], s[1], s[2])
+    return t.data_ptr(), sb, st, sh
 
 
 def _dense(name, t, dtype, shape, device):
     if t is None:
-        return None
-    if not _tensor(name, t, dtype, shape, device).is_contiguous():
+        return 0
+    _tensor(name, t, dtype, shape, device)
+    if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
-def _on(device, fn, *args):
-    """fn(*args, stream) on the current stream of `device`, with that device current."""
+def _on(device, name, *args):
+    """The library's `name`(*args, stream) on the current stream of `device`, with that device
+    current; raises for a status that is not OK."""
     torch = _torch()
     if device.type != "cuda":
         raise ValueError(f"tensors must be on a CUDA device, not on {device}")
-    if device.index == torch.cuda.current_device():
-        return fn(*args, _stream())
-    with torch.cuda.device(device):
-        return fn(*args, _stream())
+    f, i = getattr(lib(), name), device.index
+    if i == torch._C._cuda_getDevice():
+        st = f(*args, torch._C._cuda_getCurrentRawStream(i))
+    else:
+        with torch.cuda.device(device):
+            st = f(*args, torch._C._cuda_getCurrentRawStream(i))
+    if st != 0:
+        _check(name, st)
+
+
+def _four(name, t):
+    if t.dim() != 4:
+        raise ValueError(f"{name} must be [B, T, H, D], got {tuple(t.shape)}")
+    return t.shape
 
 
 def qk_norm_rope(q, k, q_gamma=None, k_gamma=None, table=None, positions=None, eps=1e-6, pairs="half", norm=True,
@@ -517,52 +558,52 @@ def qk_norm_rope(q, k, q_gamma=None, k_gamma=None, table=None, positions=None, e
     (2i, 2i + 1); positions int32 [B, T] (None: start[b] + t); norm=False: no norm.
     With cache, k and v [B, T, Hkv, D] are quantized into its rows start[b] + t (start int32 [B],
     None: 0) instead, and the result is (q_out, cache).  count int32 [B]: the tokens of each
-    sequence; the others' outputs and rows are left as they were."""
+    sequence; the others' outputs and rows are left as they were (new tensors: undefined)."""
     torch = _torch()
     ref = q if q is not None else k
     if ref is None:
         raise ValueError("q and k are both missing")
     if pairs not in PAIRS:
         raise ValueError(f"pairs must be 'half' or 'inter', got {pairs!r}")
-    if ref.dim() != 4:
-        raise ValueError(f"q and k must be [B, T, H, D], got {tuple(ref.shape)}")
-    (B, T, _, D), dev = ref.shape, ref.device
-    a = _QkArgs(B=B, T=T, D=D, pairs=PAIRS[pairs], norm=int(bool(norm)), eps=eps)
+    B, T, Hq, D = _four("q" if q is not None else "k", ref)
+    dev, i32 = ref.device, torch.int32
+    hq = hk = hv = hqo = hko = _NO_HEADS
+    Hkv = R = rows = 0
     if q is not None:
-        a.Hq = q.shape[2]
-        a.q = _heads("q", q, (B, T, a.Hq, D), dev)
+        hq = _heads("q", q, ref.shape, dev)
         if q_out is None:
-            q_out = torch.empty((B, T, a.Hq, D), dtype=torch.bfloat16, device=dev)
-        a.q_out = _heads("q_out", q_out, (B, T, a.Hq, D), dev)
+            q_out = torch.empty(ref.shape, dtype=torch.bfloat16, device=dev)
+        hqo = _heads("q_out", q_out, ref.shape, dev)
+    else:
+        Hq = 0
     if k is not None:
-        if k.dim() != 4:
-            raise ValueError(f"k must be [B, T, H, D], got {tuple(k.shape)}")
-        a.Hkv = k.shape[2]
-        a.k = _heads("k", k, (B, T, a.Hkv, D), dev)
+        Hkv = _four("k", k)[2]
+        shape = (B, T, Hkv, D)
+        hk = _heads("k", k, shape, dev)
         if cache is None:
             if k_out is None:
-                k_out = torch.empty((B, T, a.Hkv, D), dtype=torch.bfloat16, device=dev)
-            a.k_out = _heads("k_out", k_out, (B, T, a.Hkv, D), dev)
+                k_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+            hko = _heads("k_out", k_out, shape, dev)
     if cache is not None:
         if k is None or v is None or k_out is not None:
             raise ValueError("with a cache, k and v are needed, and there is no k_out")
-        a.v = _heads("v", v, (B, T, a.Hkv, D), dev)
+        hv = _heads("v", v, shape, dev)
         if cache.k_codes.device != dev:
             raise ValueError(f"cache is on {cache.k_codes.device}, not on {dev}")
-        c = cache.c()
-        a.cache = C.pointer(c)
     elif v is not None:
         raise ValueError("v is taken with a cache only")
-    a.q_gamma = _dense("q_gamma", q_gamma, torch.bfloat16, (D,), dev)
-    a.k_gamma = _dense("k_gamma", k_gamma, torch.bfloat16, (D,), dev)
     if table is not None:
-        a.table = _dense("table", table, torch.float32, table.shape, dev)
-        a.table_rows, a.R = table.shape
-    a.positions = _dense("positions", positions, torch.int32, (B, T), dev)
-    a.start = _dense("start", start, torch.int32, (B,), dev)
-    a.count = _dense("count", count, torch.int32, (B,), dev)
-    _check("nvfp4_qk_norm_rope", _on(dev, lib().nvfp4_qk_norm_rope, C.byref(a)))
-    return q_out, (cache if cache is not None else k_out)
+        if table.dim() != 2:
+            raise ValueError(f"table must be [rows, R], got {tuple(table.shape)}")
+        rows, R = table.shape
+    a = _PACK_QK.pack(
+        B, T, Hq, Hkv, D, R, PAIRS[pairs], 1 if norm else 0, eps, *hq, *hk, *hv, *hqo, *hko,
+        _dense("q_gamma", q_gamma, torch.bfloat16, (D,), dev), _dense("k_gamma", k_gamma, torch.bfloat16, (D,), dev),
+        0 if table is None else _dense("table", table, torch.float32, (rows, R), dev), rows,
+        _dense("positions", positions, i32, (B, T), dev), _dense("start", start, i32, (B,), dev),
+        _dense("count", count, i32, (B,), dev), *(_NO_CACHE if cache is None else cache.c()), cache is not None)
+    _on(dev, "nvfp4_qk_norm_rope", a)
+    return q_out, (k_out if cache is None else cache)
 
 
 def kv_write(cache: KVCache, k, v, start=None, count=None) -> KVCache:
@@ -577,13 +618,13 @@ def kv_read(cache: KVCache, start=None, length=None, k_out=None, v_out=None):
     all rows) as bf16 (k, v), each [B, length, H, D]."""
     torch = _torch()
     c, dev = cache.c(), cache.k_codes.device
-    length = c.length if length is None else length
-    shape = (c.B, length, c.H, c.D)
-    k_out = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k_out is None else k_out
-    v_out = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v_out is None else v_out
-    st = _on(dev, lib().nvfp4_kv_read, C.byref(c), _dense("start", start, torch.int32, (c.B,), dev), length,
-             _heads("k_out", k_out, shape, dev), _heads("v_out", v_out, shape, dev))
-    _check("nvfp4_kv_read", st)
+    shape = (c[6], c[10] if length is None else length, c[7], c[9])
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    _on(dev, "nvfp4_kv_read", _PACK_CACHE.pack(*c), _dense("start", start, torch.int32, (c[6],), dev), shape[1],
+        _Heads(*_heads("k_out", k_out, shape, dev)), _Heads(*_heads("v_out", v_out, shape, dev)))
     return k_out, v_out
 
 
@@ -596,41 +637,39 @@ def attention(q, k=None, v=None, cache: Optional[KVCache] = None, kv_len=None, k
     leaves a key out.  A query without keys gives 0.  scale defaults to 1/sqrt(D).
     workspace: scratch, grown on demand; None takes it from the allocator for this call."""
     torch = _torch()
-    if q.dim() != 4:
-        raise ValueError(f"q must be [B, T, Hq, D], got {tuple(q.shape)}")
-    (B, T, Hq, D), dev = q.shape, q.device
-    a = _AttentionArgs(B=B, T=T, Hq=Hq, D=D, scale=D ** -0.5 if scale is None else scale)
-    a.q = _heads("q", q, (B, T, Hq, D), dev)
+    shape = B, T, Hq, D = _four("q", q)
+    dev = q.device
+    hk = hv = _NO_HEADS
     if cache is not None:
         if k is not None or v is not None:
             raise ValueError("keys come from k and v or from a cache, not from both")
         if cache.k_codes.device != dev:
             raise ValueError(f"cache is on {cache.k_codes.device}, not on {dev}")
         c = cache.c()
-        a.S, a.Hkv, a.cache = c.length, c.H, C.pointer(c)
+        S, Hkv = c[10], c[7]
     else:
         if k is None or v is None:
             raise ValueError("k and v, or a cache, are needed")
-        if k.dim() != 4:
-            raise ValueError(f"k must be [B, S, Hkv, D], got {tuple(k.shape)}")
-        a.S, a.Hkv = k.shape[1], k.shape[2]
-        a.k = _heads("k", k, (B, a.S, a.Hkv, D), dev)
-        a.v = _heads("v", v, (B, a.S, a.Hkv, D), dev)
+        c, (_, S, Hkv, _) = _NO_CACHE, _four("k", k)
+        hk, hv = _heads("k", k, (B, S, Hkv, D), dev), _heads("v", v, (B, S, Hkv, D), dev)
     if out is None:
-        out = torch.empty((B, T, Hq, D), dtype=torch.bfloat16, device=dev)
-    a.out = _heads("out", out, (B, T, Hq, D), dev)
-    a.kv_len = _dense("kv_len", kv_len, torch.int32, (B,), dev)
+        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    mask = mask_stride = 0
     if key_mask is not None:
-        _tensor("key_mask", key_mask, torch.bool if key_mask.dtype == torch.bool else torch.uint8, (B, a.S), dev)
-        if a.S > 1 and key_mask.stride(1) != 1:
+        _tensor("key_mask", key_mask, torch.bool if key_mask.dtype is torch.bool else torch.uint8, (B, S), dev)
+        mask_stride, step = key_mask.stride()
+        if S > 1 and step != 1:
             raise ValueError("key_mask: the places of a sequence must be adjacent")
-        a.key_mask, a.mask_stride = key_mask.data_ptr(), key_mask.stride(0)
-    need = lib().nvfp4_attention_workspace_bytes(C.byref(a))
+        mask = key_mask.data_ptr()
+    a = _PACK_ATTENTION.pack(
+        B, T, S, Hq, Hkv, D, D ** -0.5 if scale is None else scale, *_heads("q", q, shape, dev), *hk, *hv,
+        *_heads("out", out, shape, dev), _dense("kv_len", kv_len, torch.int32, (B,), dev), mask, mask_stride, *c,
+        cache is not None)
+    ws, need = None, lib().nvfp4_attention_workspace_bytes(a)
     if need:
-        if workspace is not None:
-            ws, a.ws_bytes = workspace.get(need)
+        if workspace is None:
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
         else:
-            ws, a.ws_bytes = torch.empty(need, dtype=torch.uint8, device=dev), need
-        a.workspace = ws.data_ptr()
-    _check("nvfp4_attention", _on(dev, lib().nvfp4_attention, C.byref(a)))
+            ws, need = workspace.get(need)
+    _on(dev, "nvfp4_attention", a, None if ws is None else ws.data_ptr(), need)
     return out
