@@ -6,7 +6,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libnvfp4.so")
 SOURCES = ["api.cu", "gemm.cu", "gemm_persistent.cu", "gemm_grouped.cu", "norm_quant.cu", "mma_rate.cu",
-           "qk_norm_rope.cu", "kv_cache.cu", "attention.cu", "attention_tiles.cu", "attention_rows.cu"]
+           "qk_norm_rope.cu", "kv_cache.cu", "attention_join.cu", "attention_tiles.cu", "attention_rows.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
          "-Xcompiler", "-fPIC", "-shared", "--threads", "0", "--expt-relaxed-constexpr", "-Xcompiler", "-Wall"]

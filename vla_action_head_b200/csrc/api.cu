@@ -496,10 +496,9 @@ bool attention_few_rows(const AttnArgs &a) { return static_cast<long long>(a.T) 
 // Parts of the key range: the number of least modelled time (us).
 int attention_splits(const AttnArgs &a) {
     const bool few = attention_few_rows(a);
-    const int slots = sm_count_cached() * (!few && a.D <= 128 ? 2 : 1);
+    const int slots = sm_count_cached() * (!few && !a.cached && a.D <= 128 ? 2 : 1);
     const long long tiles = (few ? 1 : (static_cast<long long>(a.T) * a.G + 127) / 128) * a.B * a.Hkv;
-    const int unit = few ? 128 : 128;  // keys of a step of a CTA
-    const int keys = (a.S + unit - 1) / unit;
+    const int keys = (a.S + 127) / 128;  // tiles, or steps of 8 warps
     const double each = few ? (a.cached ? 0.8 : 3.0) * a.D / 256.0 : 1.2;
     int best = 1;
     double best_cost = 1e300;
@@ -564,7 +563,7 @@ nvfp4_status attention_args(const nvfp4_attention_args &x, AttnArgs *a, bool *em
     a->k_mul_b = a->k.sb != 0;
     a->v_mul_h = a->v.sh != 0;
     a->v_mul_b = a->v.sb != 0;
-    a->splits = a->cached && !attention_few_rows(*a) ? 1 : attention_splits(*a);
+    a->splits = attention_splits(*a);
     return NVFP4_OK;
 }
 
@@ -1100,17 +1099,15 @@ nvfp4_status nvfp4_attention(const nvfp4_attention_args *x, void *workspace, siz
     cudaError_t e;
     if (attention_few_rows(a)) {
         e = launch_attention_rows(a, stream);
-        if (e == cudaSuccess && a.splits > 1) e = launch_attention_join(a, stream);
-    } else if (a.cached || a.S == 0) {
-        e = launch_attention(a, stream);
     } else {
-        CUtensorMap mk, mv;
-        if (!make_kv_map(&mk, a.k, a.D, a.Hkv, a.S, a.B, 128) ||
-            !make_kv_map(&mv, a.v, a.D, a.Hkv, a.S, a.B, attention_v_box_rows(a.D)))
+        CUtensorMap mk = {}, mv = {};
+        if (!a.cached && a.S > 0 &&
+            (!make_kv_map(&mk, a.k, a.D, a.Hkv, a.S, a.B, 128) ||
+             !make_kv_map(&mv, a.v, a.D, a.Hkv, a.S, a.B, attention_v_box_rows(a.D))))
             return NVFP4_ERR_CUDA;
         e = launch_attention_tiles(mk, mv, a, stream);
-        if (e == cudaSuccess && a.splits > 1) e = launch_attention_join(a, stream);
     }
+    if (e == cudaSuccess && a.splits > 1) e = launch_attention_join(a, stream);
     if (e == cudaSuccess) e = cudaGetLastError();
     return from_cuda(e);
 }

@@ -1,5 +1,5 @@
 // attention.h — internal interface between the C ABI (api.cu) and the attention-side kernels
-// (qk_norm_rope.cu, kv_cache.cu, attention.cu).
+// (qk_norm_rope.cu, kv_cache.cu, attention_*.cu).
 #pragma once
 
 #include <cuda.h>
@@ -65,7 +65,6 @@ struct AttnArgs {
     float2 *part_ml; // [rows of all heads, splits]: reference in units of log2, sum of weights
     uint32_t *status;
 };
-cudaError_t launch_attention(const AttnArgs &a, cudaStream_t s);
 cudaError_t launch_attention_join(const AttnArgs &a, cudaStream_t s);
 cudaError_t probe_attention();
 

@@ -60,27 +60,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-// A UE4M3 scale byte -> the fp16 pair (s, s), exact.
-__device__ __forceinline__ uint32_t scale_f16x2(uint32_t byte) {
-    uint32_t r;
-    asm("{\n\t.reg .b16 h;\n\t"
-        "cvt.u16.u32 h, %1;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, h;\n\t}"
-        : "=r"(r)
-        : "r"(byte * 0x0101u));
-    return r;
-}
-
 template <int BYTES>
 __device__ __forceinline__ void copy_async(uint32_t dst, const void *src, bool on) {
     const uint32_t n = on ? BYTES : 0u;  // 0: zeros
@@ -263,10 +242,7 @@ __global__ void __launch_bounds__(Cfg<DP, FULL, CACHED>::kThreads, 1) attention_
             }
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // the largest element to [2^14, 2^15); infinities, NaN and zero rows as they are
-            const int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-            const int sh = (top > 0.0f && top < INFINITY) ? min(max(14 - ex, -113), 126) : 0;
-            const float up = __uint_as_float(static_cast<uint32_t>(sh + 127) << 23);
+            const float up = f16_row_factor(top);
 #pragma unroll
             for (int i = 0; i < kKRun / 8; ++i) {
                 uint32_t h[4];
@@ -275,7 +251,7 @@ __global__ void __launch_bounds__(Cfg<DP, FULL, CACHED>::kThreads, 1) attention_
                 for (int k = 0; k < 4; ++k) q[2 * i + k / 2][k & 1] = pack_f16x2(bf16lo(h[k]) * up, bf16hi(h[k]) * up);
             }
             // this thread's score columns are rows 2t and 2t + 1: their factors come below
-            sm_m[warp][g] = __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);  // 4 equal writes
+            sm_m[warp][g] = 1.0f / up;  // 4 equal writes
         } else {
 #pragma unroll
             for (int i = 0; i < kKRun / 8; ++i) {

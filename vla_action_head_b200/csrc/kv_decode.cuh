@@ -39,4 +39,34 @@ __device__ __forceinline__ void decode_e2m1x8(uint32_t codes, float (&y)[8]) {
     }
 }
 
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// A UE4M3 scale byte -> the fp16 pair (s, s), exact.
+__device__ __forceinline__ uint32_t scale_f16x2(uint32_t byte) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 h;\n\t"
+        "cvt.u16.u32 h, %1;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, h;\n\t}"
+        : "=r"(r)
+        : "r"(byte * 0x0101u));
+    return r;
+}
+
+// The power of two that brings a row whose largest magnitude is `top` to [2^14, 2^15), so that bf16
+// becomes fp16 without losing a bit that matters; 1 for rows of zeros, infinities or NaN.  Its
+// inverse is a normal number.
+__device__ __forceinline__ float f16_row_factor(float top) {
+    const int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+    const int sh = (top > 0.0f && top < INFINITY) ? min(max(14 - ex, -113), 126) : 0;
+    return __uint_as_float(static_cast<uint32_t>(sh + 127) << 23);
+}
+
 }  // namespace nvfp4

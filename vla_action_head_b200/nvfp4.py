@@ -497,49 +497,61 @@ def empty_kv_cache(B, length, H, D, device="cuda", k_scale=1.0, v_scale=1.0) -> 
     return KVCache(*bufs, k_scale, v_scale, length)
 
 
-def _tensor(name, t, dtype, shape, device):
+# These run on every call of a path whose kernels take microseconds, so the good case is one
+# comparison each and the reasons are looked for afterwards.
+def _refuse(name, t, dtype, shape, device):
+    if t is None:
+        raise ValueError(f"{name} is missing")
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    raise ValueError(f"{name} is on {t.device}, not on {device}")
 
 
 def _heads(name, t, shape, device):
     """The fields of an nvfp4_heads for a bf16 [B, T, H, D] view, the elements of a head adjacent."""
-    if t is None:
-        raise ValueError(f"{name} is missing")
-    _tensor(name, t, _torch().bfloat16, shape, device)
+    if t is None or t.dtype is not _torch_module.bfloat16 or t.shape != shape or t.device != device:
+        _refuse(name, t, _torch().bfloat16, shape, device)
     sb, st, sh, sd = t.stride()
     if sd != 1 and shape[3] > 1:
         raise ValueError(f"{name}: the elements of a head must be adjacent")
     return t.data_ptr(), sb, st, sh
 
 
+def _out_heads(name, t, shape, device):
+    """An output of `shape` (new and dense if not given) and its nvfp4_heads fields."""
+    if t is not None:
+        return t, _heads(name, t, shape, device)
+    _, T, H, D = shape
+    t = _torch_module.empty_strided(shape, (T * H * D, H * D, D, 1), dtype=_torch_module.bfloat16, device=device)
+    return t, (t.data_ptr(), T * H * D, H * D, D)
+
+
 def _dense(name, t, dtype, shape, device):
     if t is None:
         return 0
-    _tensor(name, t, dtype, shape, device)
+    if t.dtype is not dtype or t.shape != shape or t.device != device:
+        _refuse(name, t, dtype, shape, device)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
-def _on(device, name, *args):
-    """The library's `name`(*args, stream) on the current stream of `device`, with that device
+def _on(device, f, *args):
+    """The library function f(*args, stream) on the current stream of `device`, with that device
     current; raises for a status that is not OK."""
-    torch = _torch()
-    if device.type != "cuda":
+    i = device.index
+    if i is None or device.type != "cuda":
         raise ValueError(f"tensors must be on a CUDA device, not on {device}")
-    f, i = getattr(lib(), name), device.index
-    if i == torch._C._cuda_getDevice():
-        st = f(*args, torch._C._cuda_getCurrentRawStream(i))
+    cuda = _torch_module._C
+    if i == cuda._cuda_getDevice():
+        st = f(*args, cuda._cuda_getCurrentRawStream(i))
     else:
-        with torch.cuda.device(device):
-            st = f(*args, torch._C._cuda_getCurrentRawStream(i))
+        with _torch_module.cuda.device(device):
+            st = f(*args, cuda._cuda_getCurrentRawStream(i))
     if st != 0:
-        _check(name, st)
+        _check(f.__name__, st)
 
 
 def _four(name, t):
@@ -565,15 +577,13 @@ def qk_norm_rope(q, k, q_gamma=None, k_gamma=None, table=None, positions=None, e
         raise ValueError("q and k are both missing")
     if pairs not in PAIRS:
         raise ValueError(f"pairs must be 'half' or 'inter', got {pairs!r}")
-    B, T, Hq, D = _four("q" if q is not None else "k", ref)
+    B, T, Hq, D = shape = _four("q" if q is not None else "k", ref)
     dev, i32 = ref.device, torch.int32
     hq = hk = hv = hqo = hko = _NO_HEADS
     Hkv = R = rows = 0
     if q is not None:
-        hq = _heads("q", q, ref.shape, dev)
-        if q_out is None:
-            q_out = torch.empty(ref.shape, dtype=torch.bfloat16, device=dev)
-        hqo = _heads("q_out", q_out, ref.shape, dev)
+        hq = _heads("q", q, shape, dev)
+        q_out, hqo = _out_heads("q_out", q_out, shape, dev)
     else:
         Hq = 0
     if k is not None:
@@ -581,9 +591,7 @@ def qk_norm_rope(q, k, q_gamma=None, k_gamma=None, table=None, positions=None, e
         shape = (B, T, Hkv, D)
         hk = _heads("k", k, shape, dev)
         if cache is None:
-            if k_out is None:
-                k_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-            hko = _heads("k_out", k_out, shape, dev)
+            k_out, hko = _out_heads("k_out", k_out, shape, dev)
     if cache is not None:
         if k is None or v is None or k_out is not None:
             raise ValueError("with a cache, k and v are needed, and there is no k_out")
@@ -602,7 +610,7 @@ def qk_norm_rope(q, k, q_gamma=None, k_gamma=None, table=None, positions=None, e
         0 if table is None else _dense("table", table, torch.float32, (rows, R), dev), rows,
         _dense("positions", positions, i32, (B, T), dev), _dense("start", start, i32, (B,), dev),
         _dense("count", count, i32, (B,), dev), *(_NO_CACHE if cache is None else cache.c()), cache is not None)
-    _on(dev, "nvfp4_qk_norm_rope", a)
+    _on(dev, lib().nvfp4_qk_norm_rope, a)
     return q_out, (k_out if cache is None else cache)
 
 
@@ -619,12 +627,10 @@ def kv_read(cache: KVCache, start=None, length=None, k_out=None, v_out=None):
     torch = _torch()
     c, dev = cache.c(), cache.k_codes.device
     shape = (c[6], c[10] if length is None else length, c[7], c[9])
-    if k_out is None:
-        k_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-    if v_out is None:
-        v_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-    _on(dev, "nvfp4_kv_read", _PACK_CACHE.pack(*c), _dense("start", start, torch.int32, (c[6],), dev), shape[1],
-        _Heads(*_heads("k_out", k_out, shape, dev)), _Heads(*_heads("v_out", v_out, shape, dev)))
+    k_out, hk = _out_heads("k_out", k_out, shape, dev)
+    v_out, hv = _out_heads("v_out", v_out, shape, dev)
+    _on(dev, lib().nvfp4_kv_read, _PACK_CACHE.pack(*c), _dense("start", start, torch.int32, (c[6],), dev), shape[1],
+        _Heads(*hk), _Heads(*hv))
     return k_out, v_out
 
 
@@ -639,7 +645,7 @@ def attention(q, k=None, v=None, cache: Optional[KVCache] = None, kv_len=None, k
     torch = _torch()
     shape = B, T, Hq, D = _four("q", q)
     dev = q.device
-    hk = hv = _NO_HEADS
+    hq, hk, hv = _heads("q", q, shape, dev), _NO_HEADS, _NO_HEADS
     if cache is not None:
         if k is not None or v is not None:
             raise ValueError("keys come from k and v or from a cache, not from both")
@@ -652,18 +658,18 @@ def attention(q, k=None, v=None, cache: Optional[KVCache] = None, kv_len=None, k
             raise ValueError("k and v, or a cache, are needed")
         c, (_, S, Hkv, _) = _NO_CACHE, _four("k", k)
         hk, hv = _heads("k", k, (B, S, Hkv, D), dev), _heads("v", v, (B, S, Hkv, D), dev)
-    if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    out, ho = _out_heads("out", out, shape, dev)
     mask = mask_stride = 0
     if key_mask is not None:
-        _tensor("key_mask", key_mask, torch.bool if key_mask.dtype is torch.bool else torch.uint8, (B, S), dev)
+        kind = torch.bool if key_mask.dtype is torch.bool else torch.uint8
+        if key_mask.dtype is not kind or key_mask.shape != (B, S) or key_mask.device != dev:
+            _refuse("key_mask", key_mask, kind, (B, S), dev)
         mask_stride, step = key_mask.stride()
         if S > 1 and step != 1:
             raise ValueError("key_mask: the places of a sequence must be adjacent")
         mask = key_mask.data_ptr()
     a = _PACK_ATTENTION.pack(
-        B, T, S, Hq, Hkv, D, D ** -0.5 if scale is None else scale, *_heads("q", q, shape, dev), *hk, *hv,
-        *_heads("out", out, shape, dev), _dense("kv_len", kv_len, torch.int32, (B,), dev), mask, mask_stride, *c,
+        B, T, S, Hq, Hkv, D, D ** -0.5 if scale is None else scale, *hq, *hk, *hv, *ho, _dense("kv_len", kv_len, torch.int32, (B,), dev), mask, mask_stride, *c,
         cache is not None)
     ws, need = None, lib().nvfp4_attention_workspace_bytes(a)
     if need:
@@ -671,5 +677,5 @@ def attention(q, k=None, v=None, cache: Optional[KVCache] = None, kv_len=None, k
             ws = torch.empty(need, dtype=torch.uint8, device=dev)
         else:
             ws, need = workspace.get(need)
-    _on(dev, "nvfp4_attention", a, None if ws is None else ws.data_ptr(), need)
+    _on(dev, lib().nvfp4_attention, a, None if ws is None else ws.data_ptr(), need)
     return out
