@@ -1020,8 +1020,8 @@ nvfp4_status nvfp4_qk_norm_rope(const nvfp4_qk_args *x, nvfp4_stream_t stream) {
         if (p != nullptr && !aligned16(p)) return NVFP4_ERR_MISALIGNED;
     for (const int32_t *p : {x->positions, x->start, x->count})
         if ((reinterpret_cast<uintptr_t>(p) & 3u) != 0) return NVFP4_ERR_MISALIGNED;
-    // one group of lanes per head and token: their number stays within a grid
-    if (static_cast<double>(x->B) * x->T * (x->Hq + 2.0 * x->Hkv) > 1.6e10) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    // heads of all tokens are counted in 31 bits
+    if (static_cast<double>(x->B) * x->T * (x->Hq + 2.0 * x->Hkv) >= 2147483648.0) return NVFP4_ERR_UNSUPPORTED_SHAPE;
     st = check_device();
     if (st != NVFP4_OK) return st;
     a.B = x->B;
@@ -1059,7 +1059,9 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache *cache, const int32_t *start, in
         st = check_heads(v_out, cache->B, length, cache->H, cache->D, true, &a.v_out);
     if (st != NVFP4_OK) return st;
     if ((reinterpret_cast<uintptr_t>(start) & 3u) != 0) return NVFP4_ERR_MISALIGNED;
-    if (static_cast<double>(cache->B) * length * cache->H > 1.6e10) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    // pieces of 8 elements are counted in 31 bits
+    if (static_cast<double>(cache->B) * length * cache->H * (cache->D / 8) >= 2147483648.0)
+        return NVFP4_ERR_UNSUPPORTED_SHAPE;
     st = check_device();
     if (st != NVFP4_OK) return st;
     a.B = cache->B;

@@ -15,6 +15,19 @@ struct Heads {
     long long sb, st, sh;
 };
 
+// Exact division of 32-bit numbers below 2^31 by a fixed divisor: a multiplication and shifts.
+struct FastDiv {
+    uint32_t d, mul, shift;
+    FastDiv() = default;
+    explicit FastDiv(uint32_t n) : d(n), mul(0), shift(0) {
+        while (shift < 32 && (1ull << shift) < n) ++shift;
+        mul = static_cast<uint32_t>(((1ull << 32) * ((1ull << shift) - n)) / n + 1);
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ uint32_t div(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
+#endif
+};
+
 // The two planes of an NVFP4 cache tensor: codes [B, H, C, D/2], scales [B, H, C, D/16].
 struct CachePlane {
     uint8_t *codes, *sf;
@@ -38,6 +51,9 @@ struct QkArgs {
     int cached;
     Cache cache;
     uint32_t *status;
+    FastDiv by_heads, by_t;  // set by the launcher
+    uint32_t items;          // heads of all tokens: below 2^31
+    double inv_d;
 };
 cudaError_t launch_qk_norm_rope(const QkArgs &a, cudaStream_t s);
 
@@ -47,6 +63,8 @@ struct ReadArgs {
     Heads k_out, v_out;  // ptr NULL: not read
     Cache cache;
     uint32_t *status;
+    FastDiv by_units, by_h, by_l;  // set by the launcher
+    uint32_t units;                // 8-element pieces of a plane's rows: below 2^31
 };
 cudaError_t launch_kv_read(const ReadArgs &a, cudaStream_t s);
 

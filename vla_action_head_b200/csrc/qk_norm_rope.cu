@@ -5,12 +5,17 @@
 //   pair (a, b) at angle i:  (a cos_i - b sin_i,  b cos_i + a sin_i)
 //   -> bf16, or per 16 elements the block quantizer of quant.cuh -> cache row start[b] + t
 //
-// One head of one token is held by a group of LPH lanes, 8 elements (16 bytes) a lane, from the
-// load to the store: read once, written once.  The sum of squares is fp64 (order-independent
-// after its one rounding to fp32, so the quantized keys do not depend on LPH); every later step
-// is a single fp32 operation in a fixed order.  A pair's other half sits R / 16 lanes away (or
-// in the same lane for adjacent pairs): its packed bf16 words come by shuffle and its norm is
-// redone, which costs half the shuffles of exchanging normed fp32 values.
+// One head of one token is held by a group of LPH lanes from the load to the store: read once,
+// written once.  The sum of squares is fp64 (order-independent after its one rounding to fp32, so
+// the quantized keys do not depend on LPH); every later step is a single fp32 operation in a fixed
+// order.  Two kernels by how a lane's elements lie:
+//   both_halves  elements 8l and D/2 + 8l: the other half of a pair (i, i + D/2) is in the same
+//                lane.  Wherever that holds: whole heads (R = D or 0) or adjacent pairs, D % 32 == 0.
+//   one_run      8 elements a lane; a pair's other half sits R / 16 lanes away: its packed bf16 words
+//                come by shuffle and its norm is redone.  Partial rotations by halves, D % 32 == 16.
+// Bound by instructions before memory: 64-bit index divisions and fp64 division and root were
+// most of one_run's 93 us for 16 x 968 tokens of 24 heads of 128 (190 MB); indexes by
+// multiplication, the root by Newton steps and both halves in a lane: XX us.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -53,32 +58,163 @@ __device__ __forceinline__ uint32_t quantize_half16(const float (&y)[8], float g
     return cvt_e2m1x8(v);
 }
 
+// A group's head of a token, and whether there is work for it.
+struct Item {
+    int b, t, h;
+    bool is_q, is_v, turns, stores, on;
+    long long row;  // cache row
+    size_t pos;     // table row
+};
+__device__ __forceinline__ Item item_of(const QkArgs &p, uint32_t item, bool first_lane) {
+    Item x;
+    x.on = item < p.items;
+    if (!x.on) item = 0;
+    const uint32_t token = p.by_heads.div(item);
+    const int h = static_cast<int>(item - token * p.by_heads.d);
+    x.b = static_cast<int>(p.by_t.div(token));
+    x.t = static_cast<int>(token - static_cast<uint32_t>(x.b) * p.by_t.d);
+    x.is_q = h < p.Hq;
+    x.is_v = h >= p.Hq + p.Hkv;
+    x.h = x.is_q ? h : x.is_v ? h - p.Hq - p.Hkv : h - p.Hq;
+    if (x.on && p.count != nullptr) x.on = x.t < __ldg(p.count + x.b);
+    x.row = (p.start != nullptr ? static_cast<long long>(__ldg(p.start + x.b)) : 0ll) + x.t;
+    const long long pos = p.positions != nullptr ? static_cast<long long>(__ldg(p.positions + token)) : x.row;
+    x.turns = p.R > 0 && !x.is_v;
+    x.stores = p.cached && !x.is_q;
+    if (x.on && ((x.turns && (pos < 0 || pos >= p.table_rows)) ||
+                 (x.stores && (x.row < 0 || x.row >= p.cache.length)))) {
+        if (first_lane) atomicCAS(p.status, static_cast<uint32_t>(kStatusOk), static_cast<uint32_t>(kStatusBadIndex));
+        x.on = false;
+    }
+    x.pos = x.on && x.turns ? static_cast<size_t>(pos) : 0;
+    return x;
+}
+
+// 1 / sqrt(m) in fp64, rounded to fp32: two Newton steps from the fp32 estimate where fp32 holds m.
+__device__ __forceinline__ float rsqrt_f64(double m) {
+    if (!(m > 1e-30 && m < 1e30)) return static_cast<float>(1.0 / sqrt(m));
+    double y = static_cast<double>(rsqrtf(static_cast<float>(m)));
+    const double h = -0.5 * m;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) y = y * __fma_rn(h * y, y, 1.5);
+    return static_cast<float>(y);
+}
+__device__ __forceinline__ double squares(const float (&x)[8], double s) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s = __fma_rn(static_cast<double>(x[i]), static_cast<double>(x[i]), s);
+    return s;
+}
+// The quantized half block of lane l into its cache row.
+__device__ __forceinline__ void store_half16(const CachePlane &c, size_t at, int D, int e, uint32_t codes,
+                                             uint32_t scale) {
+    *reinterpret_cast<uint32_t *>(c.codes + at * (D >> 1) + (e >> 1)) = codes;
+    if ((e & 8) == 0) c.sf[at * (D >> 4) + (e >> 4)] = static_cast<uint8_t>(scale);
+}
+__device__ __forceinline__ uint4 pack8(const float (&n)[8]) {
+    return make_uint4(pack_bf16x2_rn(n[0], n[1]), pack_bf16x2_rn(n[2], n[3]), pack_bf16x2_rn(n[4], n[5]),
+                      pack_bf16x2_rn(n[6], n[7]));
+}
+__device__ __forceinline__ void scale8(float (&n)[8], float r, const uint16_t *gamma) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) n[i] = __fmul_rn(n[i], r);
+    if (gamma != nullptr) {
+        float ga[8];
+        unpack8(__ldg(reinterpret_cast<const uint4 *>(gamma)), ga);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) n[i] = __fmul_rn(n[i], ga[i]);
+    }
+}
+// Four adjacent pairs by the angles at c and s.
+__device__ __forceinline__ void turn_adjacent(float (&n)[8], const float *cos, const float *sin) {
+    const float4 c = __ldg(reinterpret_cast<const float4 *>(cos)), s = __ldg(reinterpret_cast<const float4 *>(sin));
+    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float x = n[2 * i], y = n[2 * i + 1];
+        n[2 * i] = __fsub_rn(__fmul_rn(x, cc[i]), __fmul_rn(y, ss[i]));
+        n[2 * i + 1] = __fadd_rn(__fmul_rn(y, cc[i]), __fmul_rn(x, ss[i]));
+    }
+}
+
 template <int LPH>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const QkArgs p) {
+__global__ void __launch_bounds__(kThreads) qk_both_halves_kernel(const QkArgs p) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int l = threadIdx.x & (LPH - 1);
+    Item x = item_of(p, blockIdx.x * (kThreads / LPH) + threadIdx.x / LPH, l == 0);
+    const bool on = x.on && 16 * l < p.D;
+    const Heads in = x.is_q ? p.q : x.is_v ? p.v : p.k;
+    const int half = p.D >> 1, ea = 8 * l, eb = half + 8 * l;
+    uint4 ua = make_uint4(0u, 0u, 0u, 0u), ub = ua;
+    if (on) {
+        const uint16_t *src = in.ptr + x.b * in.sb + x.t * in.st + x.h * in.sh;
+        ua = __ldcg(reinterpret_cast<const uint4 *>(src + ea));
+        ub = __ldcg(reinterpret_cast<const uint4 *>(src + eb));
+    }
+    float a[8], b[8];
+    unpack8(ua, a);
+    unpack8(ub, b);
+    if (p.norm) {
+        double s = squares(b, squares(a, 0.0));
+#pragma unroll
+        for (int o = LPH / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        const float r = rsqrt_f64(__fma_rn(s, p.inv_d, static_cast<double>(p.eps)));
+        if (!x.is_v && on) {
+            const uint16_t *gamma = x.is_q ? p.q_gamma : p.k_gamma;
+            scale8(a, r, gamma != nullptr ? gamma + ea : nullptr);
+            scale8(b, r, gamma != nullptr ? gamma + eb : nullptr);
+        }
+    }
+    if (x.turns && on) {
+        const float *cs = p.table + x.pos * p.R, *sn = cs + (p.R >> 1);
+        if (p.inter) {
+            if (ea < p.R) turn_adjacent(a, cs + (ea >> 1), sn + (ea >> 1));
+            if (eb < p.R) turn_adjacent(b, cs + (eb >> 1), sn + (eb >> 1));
+        } else {  // R = D
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float4 c = __ldg(reinterpret_cast<const float4 *>(cs + ea) + j);
+                const float4 s = __ldg(reinterpret_cast<const float4 *>(sn + ea) + j);
+                const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float u = a[4 * j + i], v = b[4 * j + i];
+                    a[4 * j + i] = __fsub_rn(__fmul_rn(u, cc[i]), __fmul_rn(v, ss[i]));
+                    b[4 * j + i] = __fadd_rn(__fmul_rn(v, cc[i]), __fmul_rn(u, ss[i]));
+                }
+            }
+        }
+    }
+    if (p.cached) {
+        const CachePlane c = x.is_v ? p.cache.v : p.cache.k;
+        uint32_t sa, sb;
+        const uint32_t ca = quantize_half16(a, c.g, &sa), cb = quantize_half16(b, c.g, &sb);
+        if (x.stores) {
+            if (on) {
+                const size_t at = (static_cast<size_t>(x.b) * p.Hkv + x.h) * p.cache.C + x.row;
+                store_half16(c, at, p.D, ea, ca, sa);
+                store_half16(c, at, p.D, eb, cb, sb);
+            }
+            return;
+        }
+    }
+    if (on) {
+        const Heads out = x.is_q ? p.q_out : p.k_out;
+        uint16_t *to = out.ptr + x.b * out.sb + x.t * out.st + x.h * out.sh;
+        *reinterpret_cast<uint4 *>(to + ea) = pack8(a);
+        *reinterpret_cast<uint4 *>(to + eb) = pack8(b);
+    }
+}
+
+template <int LPH>
+__global__ void __launch_bounds__(kThreads) qk_one_run_kernel(const QkArgs p) {
     pdl_launch_dependents();
     pdl_wait();
     const int l = threadIdx.x & (LPH - 1);
     const int e0 = 8 * l;
-    const int heads = p.Hq + p.Hkv + (p.cached ? p.Hkv : 0);
-    const long long item = (static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x) / LPH;
-    const long long token = item / heads;
-    const int h = static_cast<int>(item - token * heads);
-    const int b = static_cast<int>(token / p.T), t = static_cast<int>(token - static_cast<long long>(b) * p.T);
-    const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
-    const int hh = is_q ? h : is_v ? h - p.Hq - p.Hkv : h - p.Hq;
-
-    bool on = b < p.B;
-    if (on && p.count != nullptr) on = t < __ldg(p.count + b);
-    const long long row = (on && p.start != nullptr ? static_cast<long long>(__ldg(p.start + b)) : 0ll) + t;
-    long long pos = row;
-    if (on && p.positions != nullptr) pos = __ldg(p.positions + token);
-    const bool turns = p.R > 0 && !is_v, stores = p.cached && !is_q;
-    if (on && ((turns && (pos < 0 || pos >= p.table_rows)) || (stores && (row < 0 || row >= p.cache.length)))) {
-        if (l == 0) atomicCAS(p.status, static_cast<uint32_t>(kStatusOk), static_cast<uint32_t>(kStatusBadIndex));
-        on = false;
-    }
-    on = on && e0 < p.D;
-
+    Item x = item_of(p, blockIdx.x * (kThreads / LPH) + threadIdx.x / LPH, l == 0);
+    const bool on = x.on && e0 < p.D, is_q = x.is_q, is_v = x.is_v, turns = x.turns, stores = x.stores;
+    const int b = x.b, t = x.t, hh = x.h;
     const Heads in = is_q ? p.q : is_v ? p.v : p.k;
     uint4 raw = make_uint4(0u, 0u, 0u, 0u);
     if (on) raw = __ldcg(reinterpret_cast<const uint4 *>(in.ptr + b * in.sb + t * in.st + hh * in.sh + e0));
@@ -89,42 +225,21 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const QkArgs p) 
     const uint16_t *gamma = is_q ? p.q_gamma : p.k_gamma;
     float r = 1.0f;
     if (p.norm) {
-        double s = 0.0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s = __fma_rn(static_cast<double>(n[i]), static_cast<double>(n[i]), s);
+        double s = squares(n, 0.0);
 #pragma unroll
         for (int o = LPH / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        r = static_cast<float>(1.0 / sqrt(s / p.D + static_cast<double>(p.eps)));
+        r = rsqrt_f64(__fma_rn(s, p.inv_d, static_cast<double>(p.eps)));
     }
-    const bool normed = p.norm && !is_v;
-    auto apply_norm = [&](float (&x)[8], int at) {
-        if (!normed) return;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(x[i], r);
-        if (gamma != nullptr && on) {
-            float ga[8];
-            unpack8(__ldg(reinterpret_cast<const uint4 *>(gamma + at)), ga);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(x[i], ga[i]);
-        }
+    auto apply_norm = [&](float (&y)[8], int at) {
+        if (p.norm && !is_v && on) scale8(y, r, gamma != nullptr ? gamma + at : nullptr);
     };
     apply_norm(n, e0);
 
     // ---- rotation ----
     if (p.R > 0) {
-        const float *cs = p.table + (on && turns ? pos : 0) * p.R;
+        const float *cs = p.table + x.pos * p.R;
         if (p.inter) {
-            if (turns && on && e0 < p.R) {
-                const float4 c = __ldg(reinterpret_cast<const float4 *>(cs + e0 / 2));
-                const float4 s = __ldg(reinterpret_cast<const float4 *>(cs + p.R / 2 + e0 / 2));
-                const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float x = n[2 * i], y = n[2 * i + 1];
-                    n[2 * i] = __fsub_rn(__fmul_rn(x, cc[i]), __fmul_rn(y, ss[i]));
-                    n[2 * i + 1] = __fadd_rn(__fmul_rn(y, cc[i]), __fmul_rn(x, ss[i]));
-                }
-            }
+            if (turns && on && e0 < p.R) turn_adjacent(n, cs + e0 / 2, cs + p.R / 2 + e0 / 2);
         } else {
             const int half = p.R / 2;
             const bool first = e0 < half;
@@ -160,27 +275,26 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const QkArgs p) 
         uint32_t sc;
         const uint32_t codes = quantize_half16(n, c.g, &sc);
         if (stores) {
-            if (on) {
-                const size_t at = (static_cast<size_t>(b) * p.Hkv + hh) * p.cache.C + row;
-                *reinterpret_cast<uint32_t *>(c.codes + at * (p.D >> 1) + 4 * l) = codes;
-                if ((l & 1) == 0) c.sf[at * (p.D >> 4) + (l >> 1)] = static_cast<uint8_t>(sc);
-            }
+            if (on) store_half16(c, (static_cast<size_t>(b) * p.Hkv + hh) * p.cache.C + x.row, p.D, e0, codes, sc);
             return;
         }
     }
     if (on) {
         const Heads out = is_q ? p.q_out : p.k_out;
-        *reinterpret_cast<uint4 *>(out.ptr + b * out.sb + t * out.st + hh * out.sh + e0) =
-            make_uint4(pack_bf16x2_rn(n[0], n[1]), pack_bf16x2_rn(n[2], n[3]), pack_bf16x2_rn(n[4], n[5]),
-                       pack_bf16x2_rn(n[6], n[7]));
+        *reinterpret_cast<uint4 *>(out.ptr + b * out.sb + t * out.st + hh * out.sh + e0) = pack8(n);
     }
 }
 
-template <int LPH>
-cudaError_t launch_lph(const QkArgs &a, cudaStream_t s) {
-    const long long heads = a.Hq + static_cast<long long>(a.Hkv) * (a.cached ? 2 : 1);
-    const long long ctas = (heads * a.B * a.T * LPH + kThreads - 1) / kThreads;
-    if (ctas > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+template <int LPH, bool BOTH>
+cudaError_t launch_lph(QkArgs a, cudaStream_t s) {
+    const uint32_t heads = static_cast<uint32_t>(a.Hq + a.Hkv * (a.cached ? 2 : 1));
+    a.items = heads * static_cast<uint32_t>(a.B) * static_cast<uint32_t>(a.T);
+    a.by_heads = FastDiv(heads);
+    a.by_t = FastDiv(static_cast<uint32_t>(a.T));
+    a.inv_d = 1.0 / a.D;
+    // groups of a launch: below 2^32 / LPH threads
+    const unsigned long long ctas = (static_cast<unsigned long long>(a.items) * LPH + kThreads - 1) / kThreads;
+    if (ctas > 0x7FFFFFFFull) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas));
     cfg.blockDim = dim3(kThreads);
@@ -190,18 +304,26 @@ cudaError_t launch_lph(const QkArgs &a, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl_enabled() ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<LPH>, a);
+    if constexpr (BOTH) return cudaLaunchKernelEx(&cfg, qk_both_halves_kernel<LPH>, a);
+    else return cudaLaunchKernelEx(&cfg, qk_one_run_kernel<LPH>, a);
 }
 
 }  // namespace
 
 cudaError_t launch_qk_norm_rope(const QkArgs &a, cudaStream_t s) {
-    const int lanes = a.D / 8;  // 2 .. 32, D % 16 == 0
-    if (lanes <= 2) return launch_lph<2>(a, s);
-    if (lanes <= 4) return launch_lph<4>(a, s);
-    if (lanes <= 8) return launch_lph<8>(a, s);
-    if (lanes <= 16) return launch_lph<16>(a, s);
-    return launch_lph<32>(a, s);
+    if (a.D % 32 == 0 && (a.inter || a.R == 0 || a.R == a.D)) {
+        const int lanes = a.D / 16;  // 2 .. 16
+        if (lanes <= 2) return launch_lph<2, true>(a, s);
+        if (lanes <= 4) return launch_lph<4, true>(a, s);
+        if (lanes <= 8) return launch_lph<8, true>(a, s);
+        return launch_lph<16, true>(a, s);
+    }
+    const int lanes = a.D / 8;  // 2 .. 32
+    if (lanes <= 2) return launch_lph<2, false>(a, s);
+    if (lanes <= 4) return launch_lph<4, false>(a, s);
+    if (lanes <= 8) return launch_lph<8, false>(a, s);
+    if (lanes <= 16) return launch_lph<16, false>(a, s);
+    return launch_lph<32, false>(a, s);
 }
 
 }  // namespace nvfp4
