@@ -1059,9 +1059,8 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache *cache, const int32_t *start, in
         st = check_heads(v_out, cache->B, length, cache->H, cache->D, true, &a.v_out);
     if (st != NVFP4_OK) return st;
     if ((reinterpret_cast<uintptr_t>(start) & 3u) != 0) return NVFP4_ERR_MISALIGNED;
-    // pieces of 8 elements are counted in 31 bits
-    if (static_cast<double>(cache->B) * length * cache->H * (cache->D / 8) >= 2147483648.0)
-        return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    // rows of all heads are counted in 31 bits
+    if (static_cast<double>(cache->B) * length * cache->H >= 2147483648.0) return NVFP4_ERR_UNSUPPORTED_SHAPE;
     st = check_device();
     if (st != NVFP4_OK) return st;
     a.B = cache->B;

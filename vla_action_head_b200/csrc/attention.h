@@ -52,7 +52,7 @@ struct QkArgs {
     Cache cache;
     uint32_t *status;
     FastDiv by_heads, by_t;  // set by the launcher
-    uint32_t items;          // heads of all tokens: below 2^31
+    uint32_t items;          // groups of lanes: below 2^31
     double inv_d;
 };
 cudaError_t launch_qk_norm_rope(const QkArgs &a, cudaStream_t s);
@@ -63,8 +63,7 @@ struct ReadArgs {
     Heads k_out, v_out;  // ptr NULL: not read
     Cache cache;
     uint32_t *status;
-    FastDiv by_units, by_h, by_l;  // set by the launcher
-    uint32_t units;                // 8-element pieces of a plane's rows: below 2^31
+    FastDiv by_chunks, by_h;  // set by the launcher
 };
 cudaError_t launch_kv_read(const ReadArgs &a, cudaStream_t s);
 

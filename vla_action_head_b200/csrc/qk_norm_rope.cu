@@ -30,6 +30,7 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kHeads = 2;  // of a group, where there is work for all SMs
 
 __device__ __forceinline__ void unpack8(const uint4 &u, float (&x)[8]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -58,35 +59,39 @@ __device__ __forceinline__ uint32_t quantize_half16(const float (&y)[8], float g
     return cvt_e2m1x8(v);
 }
 
-// A group's head of a token, and whether there is work for it.
+// A group's heads of a token: up to U of q, of k or of v.
 struct Item {
-    int b, t, h;
-    bool is_q, is_v, turns, stores, on;
+    int b, t, h0, n;  // n heads from h0; 0: no work
+    bool is_q, is_v, turns, stores;
     long long row;  // cache row
-    size_t pos;     // table row
+    uint32_t pos;   // table row
 };
+template <int U>
 __device__ __forceinline__ Item item_of(const QkArgs &p, uint32_t item, bool first_lane) {
     Item x;
-    x.on = item < p.items;
-    if (!x.on) item = 0;
+    const bool any = item < p.items;
+    if (!any) item = 0;
     const uint32_t token = p.by_heads.div(item);
-    const int h = static_cast<int>(item - token * p.by_heads.d);
+    int c = static_cast<int>(item - token * p.by_heads.d);
     x.b = static_cast<int>(p.by_t.div(token));
     x.t = static_cast<int>(token - static_cast<uint32_t>(x.b) * p.by_t.d);
-    x.is_q = h < p.Hq;
-    x.is_v = h >= p.Hq + p.Hkv;
-    x.h = x.is_q ? h : x.is_v ? h - p.Hq - p.Hkv : h - p.Hq;
-    if (x.on && p.count != nullptr) x.on = x.t < __ldg(p.count + x.b);
+    const int nq = (p.Hq + U - 1) / U, nk = (p.Hkv + U - 1) / U;
+    x.is_q = c < nq;
+    x.is_v = c >= nq + nk;
+    if (!x.is_q) c -= x.is_v ? nq + nk : nq;
+    x.h0 = c * U;
+    x.n = any ? min(U, (x.is_q ? p.Hq : p.Hkv) - x.h0) : 0;
+    if (p.count != nullptr && x.t >= __ldg(p.count + x.b)) x.n = 0;
     x.row = (p.start != nullptr ? static_cast<long long>(__ldg(p.start + x.b)) : 0ll) + x.t;
     const long long pos = p.positions != nullptr ? static_cast<long long>(__ldg(p.positions + token)) : x.row;
     x.turns = p.R > 0 && !x.is_v;
     x.stores = p.cached && !x.is_q;
-    if (x.on && ((x.turns && (pos < 0 || pos >= p.table_rows)) ||
-                 (x.stores && (x.row < 0 || x.row >= p.cache.length)))) {
+    if (x.n > 0 && ((x.turns && (pos < 0 || pos >= p.table_rows)) ||
+                    (x.stores && (x.row < 0 || x.row >= p.cache.length)))) {
         if (first_lane) atomicCAS(p.status, static_cast<uint32_t>(kStatusOk), static_cast<uint32_t>(kStatusBadIndex));
-        x.on = false;
+        x.n = 0;
     }
-    x.pos = x.on && x.turns ? static_cast<size_t>(pos) : 0;
+    x.pos = x.n > 0 && x.turns ? static_cast<uint32_t>(pos) : 0u;
     return x;
 }
 
@@ -99,10 +104,11 @@ __device__ __forceinline__ float rsqrt_f64(double m) {
     for (int i = 0; i < 2; ++i) y = y * __fma_rn(h * y, y, 1.5);
     return static_cast<float>(y);
 }
-__device__ __forceinline__ double squares(const float (&x)[8], double s) {
+__device__ __forceinline__ double squares(const float (&x)[8]) {
+    double s[2] = {};  // two chains
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s = __fma_rn(static_cast<double>(x[i]), static_cast<double>(x[i]), s);
-    return s;
+    for (int i = 0; i < 8; ++i) s[i & 1] = __fma_rn(static_cast<double>(x[i]), static_cast<double>(x[i]), s[i & 1]);
+    return s[0] + s[1];
 }
 // The quantized half block of lane l into its cache row.
 __device__ __forceinline__ void store_half16(const CachePlane &c, size_t at, int D, int e, uint32_t codes,
@@ -114,20 +120,19 @@ __device__ __forceinline__ uint4 pack8(const float (&n)[8]) {
     return make_uint4(pack_bf16x2_rn(n[0], n[1]), pack_bf16x2_rn(n[2], n[3]), pack_bf16x2_rn(n[4], n[5]),
                       pack_bf16x2_rn(n[6], n[7]));
 }
-__device__ __forceinline__ void scale8(float (&n)[8], float r, const uint16_t *gamma) {
+// (x r) gamma; without a gamma its words are ones, and a product with 1 changes no bit.
+__device__ __forceinline__ void scale8(float (&n)[8], float r, const uint4 &gamma) {
+    float ga[8];
+    unpack8(gamma, ga);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) n[i] = __fmul_rn(n[i], r);
-    if (gamma != nullptr) {
-        float ga[8];
-        unpack8(__ldg(reinterpret_cast<const uint4 *>(gamma)), ga);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) n[i] = __fmul_rn(n[i], ga[i]);
-    }
+    for (int i = 0; i < 8; ++i) n[i] = __fmul_rn(__fmul_rn(n[i], r), ga[i]);
 }
-// Four adjacent pairs by the angles at c and s.
-__device__ __forceinline__ void turn_adjacent(float (&n)[8], const float *cos, const float *sin) {
-    const float4 c = __ldg(reinterpret_cast<const float4 *>(cos)), s = __ldg(reinterpret_cast<const float4 *>(sin));
-    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+__device__ __forceinline__ uint4 load_gamma(const uint16_t *gamma, bool on) {
+    const uint32_t one = 0x3F803F80u;
+    return gamma != nullptr && on ? __ldg(reinterpret_cast<const uint4 *>(gamma)) : make_uint4(one, one, one, one);
+}
+// Four adjacent pairs by the angles cc and ss.
+__device__ __forceinline__ void turn_adjacent(float (&n)[8], const float *cc, const float *ss) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float x = n[2 * i], y = n[2 * i + 1];
@@ -136,73 +141,88 @@ __device__ __forceinline__ void turn_adjacent(float (&n)[8], const float *cos, c
     }
 }
 
-template <int LPH>
-__global__ void __launch_bounds__(kThreads) qk_both_halves_kernel(const QkArgs p) {
+template <int LPH, int U>
+__global__ void __launch_bounds__(kThreads, 4) qk_both_halves_kernel(const QkArgs p) {
     pdl_launch_dependents();
     pdl_wait();
     const int l = threadIdx.x & (LPH - 1);
-    Item x = item_of(p, blockIdx.x * (kThreads / LPH) + threadIdx.x / LPH, l == 0);
-    const bool on = x.on && 16 * l < p.D;
-    const Heads in = x.is_q ? p.q : x.is_v ? p.v : p.k;
+    const Item x = item_of<U>(p, blockIdx.x * (kThreads / LPH) + threadIdx.x / LPH, l == 0);
+    const bool lane_on = 16 * l < p.D && x.n > 0;
     const int half = p.D >> 1, ea = 8 * l, eb = half + 8 * l;
-    uint4 ua = make_uint4(0u, 0u, 0u, 0u), ub = ua;
-    if (on) {
-        const uint16_t *src = in.ptr + x.b * in.sb + x.t * in.st + x.h * in.sh;
-        ua = __ldcg(reinterpret_cast<const uint4 *>(src + ea));
-        ub = __ldcg(reinterpret_cast<const uint4 *>(src + eb));
-    }
-    float a[8], b[8];
-    unpack8(ua, a);
-    unpack8(ub, b);
-    if (p.norm) {
-        double s = squares(b, squares(a, 0.0));
+    uint4 ua[U], ub[U];
+    {
+        const Heads in = x.is_q ? p.q : x.is_v ? p.v : p.k;
+        const uint16_t *src = in.ptr + x.b * in.sb + x.t * in.st + x.h0 * in.sh + ea;
 #pragma unroll
-        for (int o = LPH / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        const float r = rsqrt_f64(__fma_rn(s, p.inv_d, static_cast<double>(p.eps)));
-        if (!x.is_v && on) {
-            const uint16_t *gamma = x.is_q ? p.q_gamma : p.k_gamma;
-            scale8(a, r, gamma != nullptr ? gamma + ea : nullptr);
-            scale8(b, r, gamma != nullptr ? gamma + eb : nullptr);
+        for (int u = 0; u < U; ++u, src += in.sh) {
+            ua[u] = ub[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (lane_on && u < x.n) {
+                ua[u] = __ldcg(reinterpret_cast<const uint4 *>(src));
+                ub[u] = __ldcg(reinterpret_cast<const uint4 *>(src + half));
+            }
         }
     }
-    if (x.turns && on) {
-        const float *cs = p.table + x.pos * p.R, *sn = cs + (p.R >> 1);
+    // what the heads share: gamma and the angles
+    const uint16_t *gamma = x.is_q ? p.q_gamma : p.k_gamma;
+    const uint4 ga = load_gamma(gamma + ea, gamma != nullptr && lane_on);
+    const uint4 gb = load_gamma(gamma + eb, gamma != nullptr && lane_on);
+    const bool turn_a = x.turns && lane_on && (!p.inter || ea < p.R), turn_b = x.turns && lane_on && p.inter && eb < p.R;
+    float ca[8] = {}, sa[8] = {};  // halves: the 8 angles of a and b; adjacent: a's 4, then b's 4
+    {
+        const float *cs = p.table + static_cast<size_t>(x.pos) * p.R, *sn = cs + (p.R >> 1);
+        const int i0 = p.inter ? ea >> 1 : ea, i1 = p.inter ? eb >> 1 : ea + 4;
+        if (turn_a) {
+            *reinterpret_cast<float4 *>(ca) = __ldg(reinterpret_cast<const float4 *>(cs + i0));
+            *reinterpret_cast<float4 *>(sa) = __ldg(reinterpret_cast<const float4 *>(sn + i0));
+        }
+        if (p.inter ? turn_b : turn_a) {
+            *reinterpret_cast<float4 *>(ca + 4) = __ldg(reinterpret_cast<const float4 *>(cs + i1));
+            *reinterpret_cast<float4 *>(sa + 4) = __ldg(reinterpret_cast<const float4 *>(sn + i1));
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const bool on = lane_on && u < x.n;
+        float a[8], b[8];
+        unpack8(ua[u], a);
+        unpack8(ub[u], b);
+        if (p.norm) {
+            double s = squares(a) + squares(b);
+#pragma unroll
+            for (int o = LPH / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            const float r = rsqrt_f64(__fma_rn(s, p.inv_d, static_cast<double>(p.eps)));
+            if (!x.is_v) {
+                scale8(a, r, ga);
+                scale8(b, r, gb);
+            }
+        }
         if (p.inter) {
-            if (ea < p.R) turn_adjacent(a, cs + (ea >> 1), sn + (ea >> 1));
-            if (eb < p.R) turn_adjacent(b, cs + (eb >> 1), sn + (eb >> 1));
-        } else {  // R = D
+            if (turn_a) turn_adjacent(a, ca, sa);
+            if (turn_b) turn_adjacent(b, ca + 4, sa + 4);
+        } else if (turn_a) {  // R = D
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float4 c = __ldg(reinterpret_cast<const float4 *>(cs + ea) + j);
-                const float4 s = __ldg(reinterpret_cast<const float4 *>(sn + ea) + j);
-                const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float u = a[4 * j + i], v = b[4 * j + i];
-                    a[4 * j + i] = __fsub_rn(__fmul_rn(u, cc[i]), __fmul_rn(v, ss[i]));
-                    b[4 * j + i] = __fadd_rn(__fmul_rn(v, cc[i]), __fmul_rn(u, ss[i]));
-                }
+            for (int i = 0; i < 8; ++i) {
+                const float y = a[i], z = b[i];
+                a[i] = __fsub_rn(__fmul_rn(y, ca[i]), __fmul_rn(z, sa[i]));
+                b[i] = __fadd_rn(__fmul_rn(z, ca[i]), __fmul_rn(y, sa[i]));
             }
         }
-    }
-    if (p.cached) {
-        const CachePlane c = x.is_v ? p.cache.v : p.cache.k;
-        uint32_t sa, sb;
-        const uint32_t ca = quantize_half16(a, c.g, &sa), cb = quantize_half16(b, c.g, &sb);
-        if (x.stores) {
-            if (on) {
-                const size_t at = (static_cast<size_t>(x.b) * p.Hkv + x.h) * p.cache.C + x.row;
-                store_half16(c, at, p.D, ea, ca, sa);
-                store_half16(c, at, p.D, eb, cb, sb);
+        if (p.cached && __any_sync(0xffffffffu, x.stores)) {
+            const CachePlane c = x.is_v ? p.cache.v : p.cache.k;
+            uint32_t fa, fb;
+            const uint32_t qa = quantize_half16(a, c.g, &fa), qb = quantize_half16(b, c.g, &fb);
+            if (x.stores && on) {
+                const size_t at = (static_cast<size_t>(x.b) * p.Hkv + x.h0 + u) * p.cache.C + x.row;
+                store_half16(c, at, p.D, ea, qa, fa);
+                store_half16(c, at, p.D, eb, qb, fb);
             }
-            return;
         }
-    }
-    if (on) {
-        const Heads out = x.is_q ? p.q_out : p.k_out;
-        uint16_t *to = out.ptr + x.b * out.sb + x.t * out.st + x.h * out.sh;
-        *reinterpret_cast<uint4 *>(to + ea) = pack8(a);
-        *reinterpret_cast<uint4 *>(to + eb) = pack8(b);
+        if (!x.stores && on) {
+            const Heads out = x.is_q ? p.q_out : p.k_out;
+            uint16_t *to = out.ptr + x.b * out.sb + x.t * out.st + (x.h0 + u) * out.sh;
+            *reinterpret_cast<uint4 *>(to + ea) = pack8(a);
+            *reinterpret_cast<uint4 *>(to + eb) = pack8(b);
+        }
     }
 }
 
@@ -212,9 +232,9 @@ __global__ void __launch_bounds__(kThreads) qk_one_run_kernel(const QkArgs p) {
     pdl_wait();
     const int l = threadIdx.x & (LPH - 1);
     const int e0 = 8 * l;
-    Item x = item_of(p, blockIdx.x * (kThreads / LPH) + threadIdx.x / LPH, l == 0);
-    const bool on = x.on && e0 < p.D, is_q = x.is_q, is_v = x.is_v, turns = x.turns, stores = x.stores;
-    const int b = x.b, t = x.t, hh = x.h;
+    const Item x = item_of<1>(p, blockIdx.x * (kThreads / LPH) + threadIdx.x / LPH, l == 0);
+    const bool on = x.n > 0 && e0 < p.D, is_q = x.is_q, is_v = x.is_v, turns = x.turns, stores = x.stores;
+    const int b = x.b, t = x.t, hh = x.h0;
     const Heads in = is_q ? p.q : is_v ? p.v : p.k;
     uint4 raw = make_uint4(0u, 0u, 0u, 0u);
     if (on) raw = __ldcg(reinterpret_cast<const uint4 *>(in.ptr + b * in.sb + t * in.st + hh * in.sh + e0));
@@ -225,21 +245,26 @@ __global__ void __launch_bounds__(kThreads) qk_one_run_kernel(const QkArgs p) {
     const uint16_t *gamma = is_q ? p.q_gamma : p.k_gamma;
     float r = 1.0f;
     if (p.norm) {
-        double s = squares(n, 0.0);
+        double s = squares(n);
 #pragma unroll
         for (int o = LPH / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         r = rsqrt_f64(__fma_rn(s, p.inv_d, static_cast<double>(p.eps)));
     }
     auto apply_norm = [&](float (&y)[8], int at) {
-        if (p.norm && !is_v && on) scale8(y, r, gamma != nullptr ? gamma + at : nullptr);
+        if (p.norm && !is_v) scale8(y, r, load_gamma(gamma + at, gamma != nullptr && on));
     };
     apply_norm(n, e0);
 
     // ---- rotation ----
     if (p.R > 0) {
-        const float *cs = p.table + x.pos * p.R;
+        const float *cs = p.table + static_cast<size_t>(x.pos) * p.R;
         if (p.inter) {
-            if (turns && on && e0 < p.R) turn_adjacent(n, cs + e0 / 2, cs + p.R / 2 + e0 / 2);
+            if (turns && on && e0 < p.R) {
+                float cc[4], ss[4];
+                *reinterpret_cast<float4 *>(cc) = __ldg(reinterpret_cast<const float4 *>(cs + e0 / 2));
+                *reinterpret_cast<float4 *>(ss) = __ldg(reinterpret_cast<const float4 *>(cs + p.R / 2 + e0 / 2));
+                turn_adjacent(n, cc, ss);
+            }
         } else {
             const int half = p.R / 2;
             const bool first = e0 < half;
@@ -285,9 +310,13 @@ __global__ void __launch_bounds__(kThreads) qk_one_run_kernel(const QkArgs p) {
     }
 }
 
-template <int LPH, bool BOTH>
+// U heads of a token a group (both_halves): they share the angles and gamma, and their loads are in
+// flight together; 1 where more would leave SMs without work or groups without a head.  (16 x 968
+// tokens of 24 heads of 128: 1, 2, 4 heads a group 61, 47, 52 us.)
+template <int LPH, int U, bool BOTH>
 cudaError_t launch_lph(QkArgs a, cudaStream_t s) {
-    const uint32_t heads = static_cast<uint32_t>(a.Hq + a.Hkv * (a.cached ? 2 : 1));
+    const uint32_t q = static_cast<uint32_t>((a.Hq + U - 1) / U), k = static_cast<uint32_t>((a.Hkv + U - 1) / U);
+    const uint32_t heads = q + k * (a.cached ? 2 : 1);
     a.items = heads * static_cast<uint32_t>(a.B) * static_cast<uint32_t>(a.T);
     a.by_heads = FastDiv(heads);
     a.by_t = FastDiv(static_cast<uint32_t>(a.T));
@@ -304,7 +333,7 @@ cudaError_t launch_lph(QkArgs a, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl_enabled() ? 1 : 0;
-    if constexpr (BOTH) return cudaLaunchKernelEx(&cfg, qk_both_halves_kernel<LPH>, a);
+    if constexpr (BOTH) return cudaLaunchKernelEx(&cfg, qk_both_halves_kernel<LPH, U>, a);
     else return cudaLaunchKernelEx(&cfg, qk_one_run_kernel<LPH>, a);
 }
 
@@ -313,17 +342,19 @@ cudaError_t launch_lph(QkArgs a, cudaStream_t s) {
 cudaError_t launch_qk_norm_rope(const QkArgs &a, cudaStream_t s) {
     if (a.D % 32 == 0 && (a.inter || a.R == 0 || a.R == a.D)) {
         const int lanes = a.D / 16;  // 2 .. 16
-        if (lanes <= 2) return launch_lph<2, true>(a, s);
-        if (lanes <= 4) return launch_lph<4, true>(a, s);
-        if (lanes <= 8) return launch_lph<8, true>(a, s);
-        return launch_lph<16, true>(a, s);
+        const double threads = static_cast<double>(a.B) * a.T * (a.Hq + (a.cached ? 2 : 1) * a.Hkv) * lanes;
+        const bool many = threads > 4.0 * 148 * 1024 && a.Hq % kHeads == 0 && a.Hkv % kHeads == 0;
+#define NVFP4_LANES(N) \
+    if (lanes <= N) return many ? launch_lph<N, kHeads, true>(a, s) : launch_lph<N, 1, true>(a, s);
+        NVFP4_LANES(2) NVFP4_LANES(4) NVFP4_LANES(8) NVFP4_LANES(16)
+#undef NVFP4_LANES
     }
     const int lanes = a.D / 8;  // 2 .. 32
-    if (lanes <= 2) return launch_lph<2, false>(a, s);
-    if (lanes <= 4) return launch_lph<4, false>(a, s);
-    if (lanes <= 8) return launch_lph<8, false>(a, s);
-    if (lanes <= 16) return launch_lph<16, false>(a, s);
-    return launch_lph<32, false>(a, s);
+    if (lanes <= 2) return launch_lph<2, 1, false>(a, s);
+    if (lanes <= 4) return launch_lph<4, 1, false>(a, s);
+    if (lanes <= 8) return launch_lph<8, 1, false>(a, s);
+    if (lanes <= 16) return launch_lph<16, 1, false>(a, s);
+    return launch_lph<32, 1, false>(a, s);
 }
 
 }  // namespace nvfp4
