@@ -490,6 +490,22 @@ bool make_kv_map(CUtensorMap *m, const Heads &x, int D, int H, int S, int B, int
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A map over the codes of a cache tensor as rows of D / 2 bytes, boxes of 16 rows.
+bool make_cache_map(CUtensorMap *m, const uint8_t *codes, int D, long long rows) {
+    auto fn = encode_fn();
+    if (fn == nullptr) return false;
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(D / 2), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(D / 2)};
+    cuuint32_t box[2] = {static_cast<cuuint32_t>(D / 2), 16u};
+    cuuint32_t estr[2] = {1u, 1u};
+    const CUtensorMapSwizzle swizzle = D == 256   ? CU_TENSOR_MAP_SWIZZLE_128B
+                                       : D == 128 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                  : CU_TENSOR_MAP_SWIZZLE_32B;
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(codes), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Few rows share a key head: the row kernel; else the tile kernel.
 bool attention_few_rows(const AttnArgs &a) { return static_cast<long long>(a.T) * a.G <= kAttentionRows; }
 
@@ -1098,16 +1114,18 @@ nvfp4_status nvfp4_attention(const nvfp4_attention_args *x, void *workspace, siz
     if (st != NVFP4_OK) return st;
     if ((a.status = status_word()) == nullptr) return NVFP4_ERR_CUDA;
     cudaError_t e;
-    if (attention_few_rows(a)) {
-        e = launch_attention_rows(a, stream);
-    } else {
-        CUtensorMap mk = {}, mv = {};
-        if (!a.cached && a.S > 0 &&
-            (!make_kv_map(&mk, a.k, a.D, a.Hkv, a.S, a.B, 128) ||
-             !make_kv_map(&mv, a.v, a.D, a.Hkv, a.S, a.B, attention_v_box_rows(a.D))))
+    const bool few = attention_few_rows(a);
+    CUtensorMap mk = {}, mv = {};
+    if (!a.cached && a.S > 0) {
+        if (!make_kv_map(&mk, a.k, a.D, a.Hkv, a.S, a.B, few ? 16 : 128) ||
+            !make_kv_map(&mv, a.v, a.D, a.Hkv, a.S, a.B, few ? 16 : attention_v_box_rows(a.D)))
             return NVFP4_ERR_CUDA;
-        e = launch_attention_tiles(mk, mv, a, stream);
+    } else if (few && a.S > 0 && attention_rows_mapped(a)) {
+        const long long rows = static_cast<long long>(a.B) * a.Hkv * a.cache.C;
+        if (!make_cache_map(&mk, a.cache.k.codes, a.D, rows) || !make_cache_map(&mv, a.cache.v.codes, a.D, rows))
+            return NVFP4_ERR_CUDA;
     }
+    e = few ? launch_attention_rows(mk, mv, a, stream) : launch_attention_tiles(mk, mv, a, stream);
     if (e == cudaSuccess && a.splits > 1) e = launch_attention_join(a, stream);
     if (e == cudaSuccess) e = cudaGetLastError();
     return from_cuda(e);

@@ -92,8 +92,11 @@ cudaError_t launch_attention_tiles(const CUtensorMap &mk, const CUtensorMap &mv,
 cudaError_t probe_attention_tiles();
 
 // Up to kAttentionRows (query, head) pairs per key head, keys streamed through registers.
+// Maps (steps of 16 keys): over bf16 k and v as above with boxes of 64 x 1 x 16 x 1; over a cache's
+// codes [D / 2 bytes, row], a box of 16 whole rows swizzled over their span, where attention_rows_mapped.
 constexpr int kAttentionRows = 8;
-cudaError_t launch_attention_rows(const AttnArgs &a, cudaStream_t s);
+bool attention_rows_mapped(const AttnArgs &a);
+cudaError_t launch_attention_rows(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a, cudaStream_t s);
 cudaError_t probe_attention_rows();
 
 }  // namespace nvfp4

@@ -14,16 +14,17 @@
 // Cache: codes become fp16 (exact: 2-bit significand times 4-bit scale; the weights are then fp16
 // too, closer than bf16).  Query rows are scaled by a power of two into fp16's range, which changes no bit of them.
 //
-// The loads are asynchronous copies, kStages - 1 steps of 16 keys ahead, and each thread copies just
-// what it will read itself into a place of its own: no barrier in the loop, conflict-free shared
-// memory, and 100 KB and more on their way per SM (loads into registers left one step in flight:
-// 71 us instead of XX for 8 sequences of 32701 cached keys, 256-wide heads).
+// Every warp takes steps of 16 keys of its own: its lane 0 asks the copy engine for the next step's
+// rows (a tensor copy whose 128-byte swizzle makes the reads above free of bank conflicts; plain
+// bulk copies where a cache row is no multiple of 16 bytes), and the warp waits on its own barrier.
+// No barrier of the CTA in the loop, a few instructions a step for the loads.  (8 sequences of 32701
+// cached keys, 256-wide heads: 71 us with loads into registers, 46 with cp.async by every thread, XX.)
 //
-// The warps of a CTA take turns at the steps and are joined through shared memory; one CTA takes a
-// range of keys, and the ranges of a long sequence are joined by attention_join_kernel.
+// The warps of a CTA are joined through shared memory; one CTA takes a range of keys, and the ranges
+// of a long sequence are joined by attention_join_kernel.
 // The reference m of a row is replaced only when a score outgrows it by 2^8, found by one vote a
 // step, so the steps carry no reductions; l stays per thread until the end.
-#include <cuda_fp16.h>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "attention.h"
@@ -60,20 +61,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, bool on) {
-    const uint32_t n = on ? BYTES : 0u;  // 0: zeros
-    if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n)
-                     : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {  // all but the newest N groups have landed
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
@@ -90,128 +77,135 @@ __device__ __forceinline__ uint32_t lds4(uint32_t a) {
     return v;
 }
 
-// A run of N adjacent elements of a row (from e0) as it passes through this thread's places of a
-// stage: kBytes per lane, the lanes' pieces of a copy side by side.
-//   copy: global -> shared, zeros for rows that do not exist and elements past D
-//   load: shared -> registers;  keep = 0 makes the run zero whatever its bytes are
-//   pairs(i): elements 8i .. 8i + 7 as four 16-bit pairs
-template <int N, bool FULL>
-struct CodeRun {  // NVFP4; FULL: D fills the kernel's width, so rows are aligned as runs are
-    static constexpr int kWords = N / 8, kScales = N >= 16 ? N / 16 : 1;
-    static constexpr int kPiece = N / 2 < 8 ? 4 : FULL && N / 2 >= 16 ? 16 : 8, kPieces = N / 2 / kPiece;
-    static constexpr int kScaleWords = FULL || kScales == 1 ? 1 : 2;  // a run's bytes may cross a word
-    static constexpr int kBytes = N / 2 + 4 * kScaleWords;
-    uint32_t w[kWords], s[kScales];
+__device__ __forceinline__ uint32_t lds2(uint32_t a) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds1(uint32_t a) {
+    uint16_t v;
+    asm volatile("{\n\t.reg .u32 x;\n\tld.shared.u8 x, [%1];\n\tcvt.u16.u32 %0, x;\n\t}" : "=h"(v) : "r"(a));
+    return v;
+}
 
-    __device__ __forceinline__ static void copy(uint32_t dst, int lane, const CachePlane &c, size_t row, int e0, int D,
-                                                bool on) {
-        const uint8_t *codes = c.codes + row * (D >> 1) + (e0 >> 1);
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            const bool in = on && e0 + 2 * kPiece * i < D;
-            copy_async<kPiece>(dst + i * 32 * kPiece + lane * kPiece, in ? codes + i * kPiece : c.codes, in);
-        }
-        // whole words that hold the scale bytes (the plane's size is a multiple of 16 bytes)
-        const size_t at = row * (D >> 4) + (e0 >> 4);
-        const int last = static_cast<int>(at & 3) + kScales - 1;
-        const bool in = on && e0 < D;
-        copy_async<4>(dst + 16 * N + lane * 4, in ? c.sf + (at & ~size_t(3)) : c.sf, in);
-        if constexpr (kScaleWords == 2) {
-            const bool two = in && last >= 4 && e0 + 16 * (4 - static_cast<int>(at & 3)) < D;
-            copy_async<4>(dst + 16 * N + 128 + lane * 4, two ? c.sf + (at & ~size_t(3)) + 4 : c.sf, two);
-        }
-    }
-    __device__ __forceinline__ void load(uint32_t src, int lane, size_t row, int e0, int D, bool keep) {
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            const uint32_t a = src + i * 32 * kPiece + lane * kPiece;
-            if constexpr (kPiece == 16) {
-                const uint4 u = lds16(a);
-                w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
-            } else if constexpr (kPiece == 8) {
-                const uint2 u = lds8(a);
-                w[2 * i] = u.x, w[2 * i + 1] = u.y;
-            } else {
-                w[0] = lds4(a);
-            }
-        }
-        const uint32_t off = 8u * static_cast<uint32_t>((FULL ? (e0 >> 4) : static_cast<int>(row * (D >> 4) + (e0 >> 4))) & 3);
-        uint32_t x = lds4(src + 16 * N + lane * 4);
-        if constexpr (kScaleWords == 2) x = __funnelshift_r(x, lds4(src + 16 * N + 128 + lane * 4), off);
-        else x >>= off;
-        if (!keep) x = 0u;
-#pragma unroll
-        for (int i = 0; i < kScales; ++i) s[i] = (FULL || e0 + 16 * i < D) ? (x >> (8 * i)) & 255u : 0u;
-    }
-    __device__ __forceinline__ void pairs(int i, uint32_t (&h)[4]) const {
-        decode_e2m1x8_f16(w[i], h);
-        const uint32_t sc = scale_f16x2(s[i / 2]);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) h[q] = mul_f16x2(h[q], sc);
-    }
-};
-template <int N>
-struct WideRun {  // bf16
-    static constexpr int kBytes = 2 * N;
-    uint4 u[N / 8];
-    __device__ __forceinline__ static void copy(uint32_t dst, int lane, const uint16_t *row, int e0, int D, bool on) {
-#pragma unroll
-        for (int i = 0; i < N / 8; ++i) {
-            const bool in = on && e0 + 8 * i < D;
-            copy_async<16>(dst + i * 512 + lane * 16, in ? row + e0 + 8 * i : row, in);
-        }
-    }
-    __device__ __forceinline__ void load(uint32_t src, int lane, size_t, int, int, bool keep) {
-#pragma unroll
-        for (int i = 0; i < N / 8; ++i) {
-            u[i] = lds16(src + i * 512 + lane * 16);
-            if (!keep) u[i] = make_uint4(0u, 0u, 0u, 0u);
-        }
-    }
-    __device__ __forceinline__ void load_global(const uint16_t *row, int e0, int D, bool on) {
-#pragma unroll
-        for (int i = 0; i < N / 8; ++i) {
-            u[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (on && e0 + 8 * i < D) u[i] = __ldcg(reinterpret_cast<const uint4 *>(row + e0) + i);
-        }
-    }
-    __device__ __forceinline__ void pairs(int i, uint32_t (&h)[4]) const {
-        h[0] = u[i].x, h[1] = u[i].y, h[2] = u[i].z, h[3] = u[i].w;
-    }
-};
-template <int N, bool FULL, bool CACHED>
-struct RunOf {
-    using type = CodeRun<N, FULL>;
-};
-template <int N, bool FULL>
-struct RunOf<N, FULL, false> {
-    using type = WideRun<N>;
-};
-
+// A stage of a warp holds 16 rows of K and of V.  bf16: 64-element blocks of 16 rows x 128 bytes,
+// swizzled.  Cache: 16 rows of codes (FULL, D = DP: swizzled over the row's 128, 64 or 32 bytes; else as
+// they are in the cache, D / 2 bytes a row), then the rows' D / 16 scale bytes.
 template <int DP, bool FULL, bool CACHED>
 struct Cfg {
-    using KRun = typename RunOf<DP / 4, FULL, CACHED>::type;  // of 2 keys
-    using VRun = typename RunOf<DP / 8, FULL, CACHED>::type;  // of 4 keys
-    static constexpr int kKBytes = 32 * KRun::kBytes, kVBytes = 32 * VRun::kBytes;
-    static constexpr int kStage = 2 * kKBytes + 4 * kVBytes;  // of a warp: 16 KB (bf16) or 5 KB at DP = 256
-    static constexpr int kWarps = !CACHED && DP == 256 ? 4 : 8, kThreads = 32 * kWarps;
-    static constexpr int kStages = !CACHED && DP >= 128 ? 3 : 4;
-    static constexpr int kRing = kWarps * kStages * kStage, kJoin = kWarps * kRows * DP * 4;
-    static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
-    static_assert(kSmem + 1024 <= 232448, "shared memory");
+    static constexpr int kCodes = CACHED ? 16 * DP / 2 : 16 * DP * 2;  // bytes of K's rows, and of V's
+    static constexpr int kScale = CACHED ? 16 * DP / 16 : 0;
+    static constexpr int kOffV = kCodes, kOffKs = 2 * kCodes, kOffVs = kOffKs + kScale;
+    static constexpr int kStage = (2 * (kCodes + kScale) + 1023) / 1024 * 1024;  // swizzle atoms
+    // cache: 16 warps, as turning codes into numbers is what keeps the SM busy; bf16: as many as leave
+    // two steps on their way
+    static constexpr int kWarps = CACHED ? 16 : DP == 256 ? 4 : 8, kThreads = 32 * kWarps;
+    static constexpr int kStages = CACHED ? (DP == 256 ? 2 : 3) : DP >= 128 ? 3 : 4;
+    static constexpr int kQ = DP / 16 * 256;  // Q: a step's pair of operand words per lane
+    static constexpr int kPitch = DP + 4;     // floats of a row in the join: lanes on different banks
+    static constexpr int kRing = kWarps * kStages * kStage, kJoin = kWarps * kRows * kPitch * 4;
+    static constexpr int kSmem = kQ + (kRing > kJoin ? kRing : kJoin);
+    // elements taken at a time: 16 bytes, or what a thread has of a row
+    static constexpr int kKBlock = CACHED ? (DP / 4 < 32 ? DP / 4 : 32) : 8, kKBlocks = DP / 4 / kKBlock;
+    static constexpr int kVBlock = CACHED ? DP / 8 : 8, kVBlocks = DP / 8 / kVBlock;
+    static_assert(kOffKs >= 0 && kOffVs + kScale <= kStage, "a stage's parts");
+    static_assert(kQ % 1024 == 0 && kSmem + 2048 <= 232448, "shared memory");
+    // first element of a thread's block, and of pair x of the rows of O^T
+    __device__ static int k_element(int t, int i) {
+        return CACHED ? t * (DP / 4) + i * kKBlock : (i >> 1) * 64 + (2 * t + (i & 1)) * 8;
+    }
+    __device__ static int v_element(int g, int i) { return CACHED ? g * (DP / 8) : i * 64 + g * 8; }
+    __device__ static int o_element(int g, int x) {
+        return CACHED ? g * (DP / 8) + 2 * x : (x >> 2) * 64 + g * 8 + 2 * (x & 3);
+    }
 };
 
+// 16-byte unit c of row r in rows of BYTES (a power of two) under the copy engine's swizzle of that span.
+template <int BYTES>
+__device__ __forceinline__ uint32_t swizzled(int r, int c) {
+    if constexpr (BYTES == 128) return r * 128 + ((c ^ (r & 7)) << 4);
+    else if constexpr (BYTES == 64) return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+    else return r * 32 + ((c ^ ((r >> 2) & 1)) << 4);
+}
+
+// N elements (from e) of row r of a stage's codes -> fp16 pairs; `on` = 0: zeros whatever the bytes are.
+template <int DP, bool FULL, int N>
+__device__ __forceinline__ void codes_f16(uint32_t codes, uint32_t sf, int r, int e, int D, bool on,
+                                          uint32_t (&h)[N / 2]) {
+    uint32_t w[N / 8];
+    uint32_t s = 0u;  // scale bytes; zero times any code is zero
+    if constexpr (FULL) {
+        const uint32_t a = codes + swizzled<DP / 2>(r, e >> 5) + ((e >> 1) & 15);
+        if constexpr (N == 32) {
+            const uint4 u = lds16(a);
+            w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+            s = lds2(sf + r * (DP / 16) + (e >> 4));
+        } else if constexpr (N == 16) {
+            const uint2 u = lds8(a);
+            w[0] = u.x, w[1] = u.y;
+            s = lds1(sf + r * (DP / 16) + (e >> 4));
+        } else {
+            w[0] = lds4(a);
+            s = lds1(sf + r * (DP / 16) + (e >> 4));
+        }
+    } else {
+        const uint32_t a = codes + r * (D >> 1) + (e >> 1), b = sf + r * (D >> 4) + (e >> 4);
+        if constexpr (N >= 16) {
+#pragma unroll
+            for (int i = 0; i < N / 16; ++i) {
+                w[2 * i] = w[2 * i + 1] = 0u;
+                if (e + 16 * i < D) {
+                    const uint2 u = lds8(a + 8 * i);
+                    w[2 * i] = u.x, w[2 * i + 1] = u.y;
+                    s |= lds1(b + i) << (8 * i);
+                }
+            }
+        } else {
+            w[0] = 0u;
+            if (e < D) {
+                w[0] = lds4(a);
+                s = lds1(b);
+            }
+        }
+    }
+    uint32_t sc[2];
+    scale2_f16x2(on ? s : 0u, sc[0], sc[1]);
+#pragma unroll
+    for (int q = 0; q < N / 8; ++q) {
+        uint32_t d[4];
+        decode_e2m1x8_f16(w[q], d);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) h[4 * q + k] = mul_f16x2(d[k], sc[q >> 1]);
+    }
+}
+// 8 elements: 16-byte unit c of row r of a 64-element block.
+__device__ __forceinline__ void wide_pairs(uint32_t block, int r, int c, bool on, uint32_t (&h)[4]) {
+    const uint4 u = lds16(block + swizzled<128>(r, c));
+    h[0] = on ? u.x : 0u, h[1] = on ? u.y : 0u, h[2] = on ? u.z : 0u, h[3] = on ? u.w : 0u;
+}
+
 template <int DP, bool FULL, bool CACHED>
-__global__ void __launch_bounds__(Cfg<DP, FULL, CACHED>::kThreads, 1) attention_rows_kernel(const AttnArgs p) {
+__global__ void __launch_bounds__(Cfg<DP, FULL, CACHED>::kThreads, 1)
+    attention_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                          const AttnArgs p) {
     using C = Cfg<DP, FULL, CACHED>;
     constexpr int kWarps = C::kWarps, kThreads = C::kThreads;
-    constexpr int kKRun = DP / 4, kVRun = DP / 8;  // adjacent elements of a thread
-    constexpr int kTiles = DP / 16;                // k steps of S^T, row tiles of O^T
-    extern __shared__ __align__(16) float smem_o[];  // the warps' stages, then [kWarps][kRows][DP]
-    __shared__ float sm_m[kWarps][kRows], sm_l[kWarps][kRows];
+    constexpr int kTiles = DP / 16;  // k steps of S^T, row tiles of O^T
+    extern __shared__ __align__(1024) uint8_t smem[];  // Q, then the warps' stages, then their [kRows][kPitch]
+    float *smem_o = reinterpret_cast<float *>(smem + C::kQ);
+    __shared__ float sm_m[kWarps][kRows], sm_l[kWarps][kRows], sm_q[kRows];
+    __shared__ __align__(8) uint64_t sm_bar[kWarps][C::kStages];
+    __shared__ int sm_abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const uint32_t bar = smem_u32(&sm_bar[warp][0]);
+    if (lane == 0) {
+        for (int i = 0; i < C::kStages; ++i) mbar_init(bar + 8 * i, 1);
+        fence_mbar_init();
+    }
+    if (threadIdx.x == 0) sm_abort = 0;
+    __syncwarp();
     pdl_launch_dependents();
     pdl_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     int rest = static_cast<int>(blockIdx.x);
     const int split = rest % p.splits;
     rest /= p.splits;
@@ -219,119 +213,136 @@ __global__ void __launch_bounds__(Cfg<DP, FULL, CACHED>::kThreads, 1) attention_
     const int rows = p.T * p.G;  // <= kRows
     int len = p.S;
     if (p.kv_len != nullptr) len = min(max(__ldcg(p.kv_len + b), 0), p.S);
+
+    // Q (warp 0): row g, the thread's elements of each block of K
+    constexpr int kQUnits = DP / 32;  // 8 elements each
+    uint4 qu[kQUnits];
+    if (warp == 0) {
+        const bool on = g < rows;
+        const int tq = on ? g / p.G : 0, hq = hk * p.G + (on ? g - tq * p.G : 0);
+        const uint16_t *src = p.q.ptr + b * p.q.sb + tq * p.q.st + hq * p.q.sh;
+#pragma unroll
+        for (int i = 0; i < kQUnits; ++i) {
+            const int e = C::k_element(t, i * 8 / C::kKBlock) + i * 8 % C::kKBlock;
+            qu[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (on && e < p.D) qu[i] = __ldcg(reinterpret_cast<const uint4 *>(src + e));
+        }
+    }
+
     // whole steps of 16 keys to the splits, in turn to the warps
     const int steps = (len + 15) >> 4, per = (steps + p.splits - 1) / p.splits;
     const int step0 = split * per, step1 = min(steps, step0 + per);
-
-    // Q: row g, elements of the quarter t
-    uint32_t q[kTiles][2];
-    float c = p.scale_log2;
-    {
-        const bool on = g < rows;
-        const int tq = on ? g / p.G : 0, hq = hk * p.G + (on ? g - tq * p.G : 0);
-        WideRun<kKRun> r;
-        r.load_global(p.q.ptr + b * p.q.sb + tq * p.q.st + hq * p.q.sh, t * kKRun, p.D, on);
-        if constexpr (CACHED) {
-            float top = 0.0f;
-#pragma unroll
-            for (int i = 0; i < kKRun / 8; ++i) {
-                uint32_t h[4];
-                r.pairs(i, h);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) top = fmaxf(top, fmaxf(fabsf(bf16lo(h[k])), fabsf(bf16hi(h[k]))));
-            }
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const float up = f16_row_factor(top);
-#pragma unroll
-            for (int i = 0; i < kKRun / 8; ++i) {
-                uint32_t h[4];
-                r.pairs(i, h);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) q[2 * i + k / 2][k & 1] = pack_f16x2(bf16lo(h[k]) * up, bf16hi(h[k]) * up);
-            }
-            // this thread's score columns are rows 2t and 2t + 1: their factors come below
-            sm_m[warp][g] = 1.0f / up;  // 4 equal writes
-        } else {
-#pragma unroll
-            for (int i = 0; i < kKRun / 8; ++i) {
-                uint32_t h[4];
-                r.pairs(i, h);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) q[2 * i + k / 2][k & 1] = h[k];
-            }
-        }
-    }
-    float cr[2] = {c, c};
-    if constexpr (CACHED) {
-        __syncwarp();
-        cr[0] = c * sm_m[warp][2 * t];
-        cr[1] = c * sm_m[warp][2 * t + 1];
-        __syncwarp();
-    }
-
     const uint8_t *mask = p.mask != nullptr ? p.mask + b * p.mask_stride : nullptr;
     const size_t plane = (static_cast<size_t>(b) * p.Hkv + hk) * p.cache.C;
-    const uint16_t *kbase = p.k.ptr + b * p.k.sb + hk * p.k.sh, *vbase = p.v.ptr + b * p.v.sb + hk * p.v.sh;
-    const uint32_t ring = smem_u32(smem_o) + warp * C::kStages * C::kStage;
-    // a step's keys: g, g + 8 for the scores; 2t, 2t + 1, 2t + 8, 2t + 9 for the values
-    auto copy_step = [&](int st, int slot) {
-        const uint32_t at = ring + slot * C::kStage;
-        if (st < step1) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int j = 16 * st + g + 8 * i;
-                if constexpr (CACHED) C::KRun::copy(at + i * C::kKBytes, lane, p.cache.k, plane + j, t * kKRun, p.D, j < len);
-                else C::KRun::copy(at + i * C::kKBytes, lane, j < len ? kbase + j * p.k.st : kbase, t * kKRun, p.D, j < len);
+    const uint32_t sq = smem_u32(smem), ring = sq + C::kQ + warp * C::kStages * C::kStage;
+    const int kc = (p.D + 63) >> 6;
+    const uint64_t policy = policy_evict_first();
+    auto ask = [&](int st, int slot) {  // lane 0
+        const uint32_t to = ring + slot * C::kStage, on = bar + 8 * slot;
+        if constexpr (CACHED) {
+            const size_t row = plane + 16 * static_cast<size_t>(st);
+            const uint32_t bytes = FULL ? C::kCodes : 8 * p.D;
+            mbar_arrive_expect_tx(on, 2 * bytes + 2 * p.D);
+            if constexpr (FULL) {
+                tma_load_2d(to, &map_k, 0, static_cast<int>(row), on, policy);
+                tma_load_2d(to + C::kOffV, &map_v, 0, static_cast<int>(row), on, policy);
+            } else {
+                bulk_load(to, p.cache.k.codes + row * (p.D >> 1), bytes, on, policy);
+                bulk_load(to + C::kOffV, p.cache.v.codes + row * (p.D >> 1), bytes, on, policy);
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int j = 16 * st + 2 * t + (i & 1) + 8 * (i >> 1);
-                const uint32_t to = at + 2 * C::kKBytes + i * C::kVBytes;
-                if constexpr (CACHED) C::VRun::copy(to, lane, p.cache.v, plane + j, g * kVRun, p.D, j < len);
-                else C::VRun::copy(to, lane, j < len ? vbase + j * p.v.st : vbase, g * kVRun, p.D, j < len);
+            bulk_load(to + C::kOffKs, p.cache.k.sf + row * (p.D >> 4), p.D, on, policy);
+            bulk_load(to + C::kOffVs, p.cache.v.sf + row * (p.D >> 4), p.D, on, policy);
+        } else {
+            mbar_arrive_expect_tx(on, 2 * kc * 2048);
+            for (int e = 0; e < kc; ++e) {
+                tma_load_4d(to + 2048 * e, &map_k, 64 * e, p.k_mul_h * hk, 16 * st, p.k_mul_b * b, on, policy);
+                tma_load_4d(to + C::kOffV + 2048 * e, &map_v, 64 * e, p.v_mul_h * hk, 16 * st, p.v_mul_b * b, on,
+                            policy);
             }
         }
-        copy_commit();
     };
+    if (lane == 0)
+        for (int i = 0; i < C::kStages; ++i)
+            if (step0 + warp + i * kWarps < step1) ask(step0 + warp + i * kWarps, i);
     // lane's key of a step, 1 if it is attended to; asked for one step ahead
     auto key_on = [&](int st) -> uint32_t {
         const int j = 16 * st + (lane & 15);
         if (st >= step1 || j >= len) return 0u;
         return mask == nullptr ? 1u : __ldcg(mask + j) != 0 ? 1u : 0u;
     };
+    uint32_t key = key_on(step0 + warp);
+
+    if (warp == 0) {  // Q as the operand words of each step of 16 elements
+        float up = 1.0f;
+        if constexpr (CACHED) {
+            float top = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kQUnits; ++i) {
+                const uint32_t w[4] = {qu[i].x, qu[i].y, qu[i].z, qu[i].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) top = fmaxf(top, fmaxf(fabsf(bf16lo(w[k])), fabsf(bf16hi(w[k]))));
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            up = f16_row_factor(top);
+        }
+        if (t == 0) sm_q[g] = 1.0f / up;
+#pragma unroll
+        for (int i = 0; i < kQUnits; ++i) {
+            uint32_t w[4] = {qu[i].x, qu[i].y, qu[i].z, qu[i].w};
+            if constexpr (CACHED) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[k] = pack_f16x2(bf16lo(w[k]) * up, bf16hi(w[k]) * up);
+            }
+            uint2 *to = reinterpret_cast<uint2 *>(smem) + lane;
+            to[(2 * i) * 32] = make_uint2(w[0], w[1]);
+            to[(2 * i + 1) * 32] = make_uint2(w[2], w[3]);
+        }
+    }
+    __syncthreads();
+    const float cr[2] = {p.scale_log2 * sm_q[2 * t], p.scale_log2 * sm_q[2 * t + 1]};  // of rows 2t, 2t + 1
 
     float o[kTiles][4] = {};
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};  // rows 2t, 2t + 1; m in units of log2
-#pragma unroll
-    for (int i = 0; i < C::kStages - 1; ++i) copy_step(step0 + warp + i * kWarps, i);
-    uint32_t key = key_on(step0 + warp);
     int slot = 0;
+    uint32_t phase = 0u;
     for (int st = step0 + warp; st < step1; st += kWarps) {
-        copy_wait<C::kStages - 2>();
-        copy_step(st + (C::kStages - 1) * kWarps, slot == 0 ? C::kStages - 1 : slot - 1);
         const uint32_t keys = __ballot_sync(0xffffffffu, key != 0u);
         key = key_on(st + kWarps);
-        const uint32_t at = ring + slot * C::kStage;
-        slot = slot + 1 == C::kStages ? 0 : slot + 1;
+        const bool landed = mbar_wait(bar + 8 * slot, phase, &sm_abort, p.status, kStatusTimeoutFull);
+        if (!__all_sync(0xffffffffu, landed)) {
+            // leave no copy in flight behind
+            int dummy = 0;
+            for (int i = 0; i < C::kStages && st + i * kWarps < step1; ++i) {
+                mbar_wait(bar + 8 * slot, phase, &dummy, p.status, kStatusTimeoutDrain);
+                if (++slot == C::kStages) {
+                    slot = 0;
+                    phase ^= 1u;
+                }
+            }
+            break;
+        }
+        const uint32_t at = ring + slot * C::kStage, vat = at + C::kOffV;
         const bool ok[2] = {((keys >> g) & 1u) != 0u, ((keys >> (g + 8)) & 1u) != 0u};
-        typename C::KRun kr[2];
-        typename C::VRun vr[4];
+        float sa[2][4] = {};  // two chains
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            kr[i].load(at + i * C::kKBytes, lane, plane + 16 * st + g + 8 * i, t * kKRun, p.D, true);
-        float s[4] = {};
+        for (int i = 0; i < C::kKBlocks; ++i) {
+            uint32_t h0[C::kKBlock / 2], h1[C::kKBlock / 2];
+            if constexpr (CACHED) {
+                codes_f16<DP, FULL, C::kKBlock>(at, at + C::kOffKs, g, C::k_element(t, i), p.D, true, h0);
+                codes_f16<DP, FULL, C::kKBlock>(at, at + C::kOffKs, g + 8, C::k_element(t, i), p.D, true, h1);
+            } else {
+                wide_pairs(at + (i >> 1) * 2048, g, 2 * t + (i & 1), true, h0);
+                wide_pairs(at + (i >> 1) * 2048, g + 8, 2 * t + (i & 1), true, h1);
+            }
 #pragma unroll
-        for (int i = 0; i < kKRun / 8; ++i) {
-            uint32_t h0[4], h1[4];
-            kr[0].pairs(i, h0);
-            kr[1].pairs(i, h1);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
+            for (int k = 0; k < C::kKBlock / 4; ++k) {
                 const uint32_t a[4] = {h0[2 * k], h1[2 * k], h0[2 * k + 1], h1[2 * k + 1]};
-                mma16816<CACHED>(s, a, q[2 * i + k][0], q[2 * i + k][1]);
+                const uint2 q = lds8(sq + (i * (C::kKBlock / 4) + k) * 256 + lane * 8);
+                mma16816<CACHED>(sa[k & 1], a, q.x, q.y);
             }
         }
+        const float s[4] = {sa[0][0] + sa[1][0], sa[0][1] + sa[1][1], sa[0][2] + sa[1][2], sa[0][3] + sa[1][3]};
         // scores in units of log2; left-out keys are -inf whatever their bytes gave
         float x[4];
 #pragma unroll
@@ -360,32 +371,39 @@ __global__ void __launch_bounds__(Cfg<DP, FULL, CACHED>::kThreads, 1) attention_
             w[i] = ex2(x[i] - (m[i & 1] == -INFINITY ? 0.0f : m[i & 1]));
             l[i & 1] += w[i];
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int j = 2 * t + (i & 1) + 8 * (i >> 1);
-            vr[i].load(at + 2 * C::kKBytes + i * C::kVBytes, lane, plane + 16 * st + j, g * kVRun, p.D,
-                       mask == nullptr || ((keys >> j) & 1u) != 0u);
-        }
         uint32_t pb[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
             pb[i] = transpose8x8(CACHED ? pack_f16x2(w[2 * i], w[2 * i + 1]) : pack_bf16x2_rn(w[2 * i], w[2 * i + 1]));
+        // keys 2t, 2t + 1, 2t + 8, 2t + 9; zeros for the left-out ones
 #pragma unroll
-        for (int i = 0; i < kVRun / 8; ++i) {
-            uint32_t h[4][4];
+        for (int i = 0; i < C::kVBlocks; ++i) {
+            uint32_t h[4][C::kVBlock / 2];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) vr[k].pairs(i, h[k]);
+            for (int k = 0; k < 4; ++k) {
+                const int j = 2 * t + (k & 1) + 8 * (k >> 1);
+                const bool on = ((keys >> j) & 1u) != 0u;
+                if constexpr (CACHED)
+                    codes_f16<DP, FULL, C::kVBlock>(vat, at + C::kOffVs, j, C::v_element(g, i), p.D, on, h[k]);
+                else
+                    wide_pairs(vat + i * 2048, j, g, on, h[k]);
+            }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {  // pair (e, e + 1): rows g and g + 8 of tile 4i + k
+            for (int k = 0; k < C::kVBlock / 2; ++k) {  // pair (e, e + 1): rows g and g + 8 of a tile
                 const uint32_t a[4] = {__byte_perm(h[0][k], h[1][k], 0x5410), __byte_perm(h[0][k], h[1][k], 0x7632),
                                        __byte_perm(h[2][k], h[3][k], 0x5410), __byte_perm(h[2][k], h[3][k], 0x7632)};
-                mma16816<CACHED>(o[4 * i + k], a, pb[0], pb[1]);
+                mma16816<CACHED>(o[i * (C::kVBlock / 2) + k], a, pb[0], pb[1]);
             }
+        }
+        __syncwarp();  // every lane has read the stage
+        if (lane == 0 && st + C::kStages * kWarps < step1) ask(st + C::kStages * kWarps, slot);
+        if (++slot == C::kStages) {
+            slot = 0;
+            phase ^= 1u;
         }
     }
 
-    // ---- join the warps (in the place of the stages) ----
-    copy_wait<0>();
+    // ---- join the warps (in the place of the stages; every copy asked for has been waited for) ----
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -397,46 +415,42 @@ __global__ void __launch_bounds__(Cfg<DP, FULL, CACHED>::kThreads, 1) attention_
         }
 #pragma unroll
         for (int j = 0; j < kTiles; ++j)
-            *reinterpret_cast<float2 *>(smem_o + (warp * kRows + 2 * t + i) * DP + g * kVRun + 2 * j) =
+            *reinterpret_cast<float2 *>(smem_o + (warp * kRows + 2 * t + i) * C::kPitch + 16 * j + 2 * g) =
                 make_float2(o[j][i], o[j][2 + i]);
     }
     __syncthreads();
-    constexpr int kPer = kRows * DP / kThreads;  // 2, 4, 8 or 16 adjacent elements a thread
-    const int r = threadIdx.x * kPer / DP, e0 = threadIdx.x * kPer % DP;
-    float M = -INFINITY;
+    // a thread: every kThreads-th pair of elements of the rows
+    for (int x = threadIdx.x; x < rows * (DP / 2); x += kThreads) {
+        const int r = x / (DP / 2), pair = x % (DP / 2), e = C::o_element(pair & 7, pair >> 3);
+        float M = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w)
-        if (sm_l[w][r] != 0.0f) M = fmaxf(M, sm_m[w][r]);
-    float sum = 0.0f, acc[kPer] = {};
+        for (int w = 0; w < kWarps; ++w)
+            if (sm_l[w][r] != 0.0f) M = fmaxf(M, sm_m[w][r]);
+        float sum = 0.0f, a0 = 0.0f, a1 = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (sm_l[w][r] == 0.0f) continue;
-        const float f = ex2(sm_m[w][r] - M);
-        sum = fmaf(f, sm_l[w][r], sum);
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) acc[e] = fmaf(f, smem_o[(w * kRows + r) * DP + e0 + e], acc[e]);
-    }
-    if (r >= rows) return;
-    if (p.splits > 1) {
-        const size_t at = ((static_cast<size_t>(b) * p.Hkv + hk) * rows + r) * p.splits + split;
-        if (e0 == 0) p.part_ml[at] = make_float2(M, sum);
-        if (sum != 0.0f) {
-#pragma unroll
-            for (int e = 0; e < kPer; ++e)
-                if (e0 + e < p.D) p.part_o[at * p.D + e0 + e] = acc[e];
+        for (int w = 0; w < kWarps; ++w) {
+            if (sm_l[w][r] == 0.0f) continue;
+            const float f = ex2(sm_m[w][r] - M);
+            const float2 v = *reinterpret_cast<const float2 *>(smem_o + (w * kRows + r) * C::kPitch + 2 * pair);
+            sum = fmaf(f, sm_l[w][r], sum);
+            a0 = fmaf(f, v.x, a0);
+            a1 = fmaf(f, v.y, a1);
         }
-    } else {
-        const float f = sum != 0.0f ? (CACHED ? p.cache.v.g : 1.0f) / sum : 0.0f;
-        const int tq = r / p.G, hq = hk * p.G + r - tq * p.G;
-        uint16_t *to = p.out.ptr + b * p.out.sb + tq * p.out.st + hq * p.out.sh + e0;
-#pragma unroll
-        for (int e = 0; e < kPer; e += 2)
-            if (e0 + e < p.D) *reinterpret_cast<uint32_t *>(to + e) = pack_bf16x2_rn(acc[e] * f, acc[e + 1] * f);
+        if (p.splits > 1) {
+            const size_t at = ((static_cast<size_t>(b) * p.Hkv + hk) * rows + r) * p.splits + split;
+            if (pair == 0) p.part_ml[at] = make_float2(M, sum);
+            if (sum != 0.0f && e < p.D) *reinterpret_cast<float2 *>(p.part_o + at * p.D + e) = make_float2(a0, a1);
+        } else if (e < p.D) {
+            const float f = sum != 0.0f ? (CACHED ? p.cache.v.g : 1.0f) / sum : 0.0f;
+            const int tq = r / p.G, hq = hk * p.G + r - tq * p.G;
+            *reinterpret_cast<uint32_t *>(p.out.ptr + b * p.out.sb + tq * p.out.st + hq * p.out.sh + e) =
+                pack_bf16x2_rn(a0 * f, a1 * f);
+        }
     }
 }
 
 template <int DP, bool FULL, bool CACHED>
-cudaError_t launch_rows(const AttnArgs &a, cudaStream_t s) {
+cudaError_t launch_rows(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a, cudaStream_t s) {
     static std::atomic<bool> attr_set[kMaxDevices];
     auto *kernel = attention_rows_kernel<DP, FULL, CACHED>;
     using C = Cfg<DP, FULL, CACHED>;
@@ -454,20 +468,26 @@ cudaError_t launch_rows(const AttnArgs &a, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl_enabled() ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, a);
+    return cudaLaunchKernelEx(&cfg, kernel, mk, mv, a);
 }
 template <int DP>
-cudaError_t launch_rows_dp(const AttnArgs &a, cudaStream_t s) {
-    if (!a.cached) return launch_rows<DP, false, false>(a, s);
-    return a.D == DP ? launch_rows<DP, true, true>(a, s) : launch_rows<DP, false, true>(a, s);
+cudaError_t launch_rows_dp(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a, cudaStream_t s) {
+    if (!a.cached) return launch_rows<DP, false, false>(mk, mv, a, s);
+    return attention_rows_mapped(a) ? launch_rows<DP, true, true>(mk, mv, a, s)
+                                    : launch_rows<DP, false, true>(mk, mv, a, s);
 }
 
 }  // namespace
 
-cudaError_t launch_attention_rows(const AttnArgs &a, cudaStream_t s) {
-    if (a.D <= 64) return launch_rows_dp<64>(a, s);
-    if (a.D <= 128) return launch_rows_dp<128>(a, s);
-    return launch_rows_dp<256>(a, s);
+bool attention_rows_mapped(const AttnArgs &a) {
+    return (a.D == 64 || a.D == 128 || a.D == 256) &&
+           static_cast<long long>(a.B) * a.Hkv * a.cache.C < 0x7FFFFFFFLL;
+}
+
+cudaError_t launch_attention_rows(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a, cudaStream_t s) {
+    if (a.D <= 64) return launch_rows_dp<64>(mk, mv, a, s);
+    if (a.D <= 128) return launch_rows_dp<128>(mk, mv, a, s);
+    return launch_rows_dp<256>(mk, mv, a, s);
 }
 
 cudaError_t probe_attention_rows() {

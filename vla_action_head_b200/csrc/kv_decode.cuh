@@ -28,17 +28,6 @@ __device__ __forceinline__ void decode_e2m1x8_f16(uint32_t codes, uint32_t (&h)[
         : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
         : "r"(codes));
 }
-__device__ __forceinline__ void decode_e2m1x8(uint32_t codes, float (&y)[8]) {
-    uint32_t h[4];
-    decode_e2m1x8_f16(codes, h);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[j]));
-        y[2 * j] = f.x;
-        y[2 * j + 1] = f.y;
-    }
-}
-
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -60,6 +49,17 @@ __device__ __forceinline__ uint32_t scale_f16x2(uint32_t byte) {
     return r;
 }
 
+// Two scale bytes (the low 16 bits) -> two fp16 pairs (s0, s0) and (s1, s1), exact.
+__device__ __forceinline__ void scale2_f16x2(uint32_t bytes, uint32_t &s0, uint32_t &s1) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 h;\n\t"
+        "cvt.u16.u32 h, %1;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, h;\n\t}"
+        : "=r"(r)
+        : "r"(bytes));
+    s0 = __byte_perm(r, r, 0x1010);
+    s1 = __byte_perm(r, r, 0x3232);
+}
 // The power of two that brings a row whose largest magnitude is `top` to [2^14, 2^15), so that bf16
 // becomes fp16 without losing a bit that matters; 1 for rows of zeros, infinities or NaN.  Its
 // inverse is a normal number.
