@@ -509,18 +509,16 @@ bool make_cache_map(CUtensorMap *m, const uint8_t *codes, int D, long long rows)
 // Few rows share a key head: the row kernel; else the tile kernel.
 bool attention_few_rows(const AttnArgs &a) { return static_cast<long long>(a.T) * a.G <= kAttentionRows; }
 
-// Parts of the key range: the number of least modelled time (us).
+// Tile kernel: parts of the key range, the number of least modelled time (us).
 int attention_splits(const AttnArgs &a) {
-    const bool few = attention_few_rows(a);
-    const int slots = sm_count_cached() * (!few && !a.cached && a.D <= 128 ? 2 : 1);
-    const long long tiles = (few ? 1 : (static_cast<long long>(a.T) * a.G + 127) / 128) * a.B * a.Hkv;
-    const int keys = (a.S + 127) / 128;  // tiles, or steps of 8 warps
-    const double each = few ? (a.cached ? 0.8 : 3.0) * a.D / 256.0 : 1.2;
+    const int slots = sm_count_cached() * (!a.cached && a.D <= 128 ? 2 : 1);
+    const long long tiles = (static_cast<long long>(a.T) * a.G + 127) / 128 * a.B * a.Hkv;
+    const int keys = (a.S + 127) / 128;
     int best = 1;
     double best_cost = 1e300;
     for (int s = 1; s <= keys && s <= slots && tiles * (s - 1) < 2 * slots; ++s) {
         const double waves = std::ceil(static_cast<double>(tiles * s) / slots);
-        const double cost = waves * ((keys + s - 1) / s * each + 3.0) + (s > 1 ? 3.0 + 0.05 * s : 0.0);
+        const double cost = waves * ((keys + s - 1) / s * 1.2 + 3.0) + (s > 1 ? 3.0 + 0.05 * s : 0.0);
         if (cost < best_cost) {
             best_cost = cost;
             best = s;
@@ -529,10 +527,27 @@ int attention_splits(const AttnArgs &a) {
     return best;
 }
 
-size_t attention_workspace(const AttnArgs &a) {
-    if (a.splits <= 1) return 0;
-    return static_cast<size_t>(a.B) * a.T * a.Hq * a.splits * (a.D + 2) * sizeof(float);
+// Row kernel: CTAs to deal out by the lengths, or 0: a CTA a key head (modelled time, us: a step of a
+// CTA, what a CTA costs beside its steps, and the join).
+int attention_share(const AttnArgs &a) {
+    const int sms = sm_count_cached();
+    const double segments = static_cast<double>(a.B) * a.Hkv, steps = (a.S + 15) / 16;
+    if (segments >= sms) return 0;
+    const double n = std::min(static_cast<double>(sms), segments * std::ceil(steps / a.warps));
+    if (n <= segments) return 0;
+    const double step = (a.cached ? 0.13 : 0.33) * a.D / 256.0, fixed = 4.0, join = 3.5;
+    const double whole = steps * step + fixed;
+    const double piece = std::max(std::ceil(segments * steps / (n - segments)), static_cast<double>(a.warps));
+    return piece * step + fixed + join < whole ? static_cast<int>(n) : 0;
 }
+
+// Rows of partial results in the workspace.
+size_t attention_part_rows(const AttnArgs &a) {
+    if (a.share > 0) return static_cast<size_t>(a.share) * a.T * a.G;
+    return a.splits > 1 ? static_cast<size_t>(a.B) * a.T * a.Hq * a.splits : 0;
+}
+
+size_t attention_workspace(const AttnArgs &a) { return attention_part_rows(a) * (a.D + 2) * sizeof(float); }
 
 // The arguments of nvfp4_attention, without device access; `empty`: there is nothing to write.
 nvfp4_status attention_args(const nvfp4_attention_args &x, AttnArgs *a, bool *empty) {
@@ -579,7 +594,9 @@ nvfp4_status attention_args(const nvfp4_attention_args &x, AttnArgs *a, bool *em
     a->k_mul_b = a->k.sb != 0;
     a->v_mul_h = a->v.sh != 0;
     a->v_mul_b = a->v.sb != 0;
-    a->splits = attention_splits(*a);
+    a->splits = attention_few_rows(*a) ? 1 : attention_splits(*a);
+    a->warps = attention_rows_warps(a->cached, a->D);
+    a->share = attention_few_rows(*a) ? attention_share(*a) : 0;
     return NVFP4_OK;
 }
 
@@ -1108,7 +1125,7 @@ nvfp4_status nvfp4_attention(const nvfp4_attention_args *x, void *workspace, siz
         if (workspace == nullptr || ws_bytes < need) return NVFP4_ERR_WORKSPACE;
         if (!aligned16(workspace)) return NVFP4_ERR_MISALIGNED;
         a.part_o = static_cast<float *>(workspace);
-        a.part_ml = reinterpret_cast<float2 *>(a.part_o + static_cast<size_t>(a.B) * a.T * a.Hq * a.splits * a.D);
+        a.part_ml = reinterpret_cast<float2 *>(a.part_o + attention_part_rows(a) * a.D);
     }
     st = check_device();
     if (st != NVFP4_OK) return st;
@@ -1126,7 +1143,7 @@ nvfp4_status nvfp4_attention(const nvfp4_attention_args *x, void *workspace, siz
             return NVFP4_ERR_CUDA;
     }
     e = few ? launch_attention_rows(mk, mv, a, stream) : launch_attention_tiles(mk, mv, a, stream);
-    if (e == cudaSuccess && a.splits > 1) e = launch_attention_join(a, stream);
+    if (e == cudaSuccess && need > 0) e = launch_attention_join(a, stream);
     if (e == cudaSuccess) e = cudaGetLastError();
     return from_cuda(e);
 }

@@ -77,9 +77,13 @@ struct AttnArgs {
     int cached;
     Cache cache;
     int k_mul_h, k_mul_b, v_mul_h, v_mul_b;  // 0: that dimension is broadcast, its tensor-map size 1
-    int splits;      // parts of the key range; > 1: joined from part_o and part_ml
-    float *part_o;   // [rows of all heads, splits, D]: unnormalized sums
-    float2 *part_ml; // [rows of all heads, splits]: reference in units of log2, sum of weights
+    int splits;      // tile kernel: parts of the key range; > 1: joined from part_o and part_ml
+    int share;       // row kernel: > 0: CTAs dealt out by the lengths, joined; 0: a CTA a key head
+    int warps;       // row kernel: of a CTA
+    // unnormalized sums; references in units of log2 and sums of weights.
+    // tile kernel: [rows of all heads, splits] (x D); row kernel: [CTAs, rows of a key head] (x D)
+    float *part_o;
+    float2 *part_ml;
     uint32_t *status;
 };
 cudaError_t launch_attention_join(const AttnArgs &a, cudaStream_t s);
@@ -96,6 +100,7 @@ cudaError_t probe_attention_tiles();
 // codes [D / 2 bytes, row], a box of 16 whole rows swizzled over their span, where attention_rows_mapped.
 constexpr int kAttentionRows = 8;
 bool attention_rows_mapped(const AttnArgs &a);
+int attention_rows_warps(bool cached, int D);
 cudaError_t launch_attention_rows(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a, cudaStream_t s);
 cudaError_t probe_attention_rows();
 

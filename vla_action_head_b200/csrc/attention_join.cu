@@ -2,6 +2,7 @@
 #include <cuda_runtime.h>
 
 #include "attention.h"
+#include "attention_share.cuh"
 #include "gemm.h"
 #include "quant.cuh"
 #include "sm100.cuh"
@@ -12,8 +13,9 @@ namespace {
 
 constexpr int kThreads = 128;
 
-// Joins the parts of a split key range: with M the largest reference of the parts that have a sum,
-// out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s (references in units of log2), in the order of s.  A warp a row.
+// A warp a row: with M the largest reference of the parts that have a sum,
+// out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s (references in units of log2), in the order of s.
+// The factors are found 32 parts at a time, a part a lane; the sums' loads do not wait for one another.
 __global__ void __launch_bounds__(kThreads) attention_join_kernel(const AttnArgs p) {
     pdl_launch_dependents();
     pdl_wait();
@@ -23,30 +25,50 @@ __global__ void __launch_bounds__(kThreads) attention_join_kernel(const AttnArgs
     const int rows = p.T * p.G;
     const int r = static_cast<int>(row % rows), bh = static_cast<int>(row / rows);
     const int hk = bh % p.Hkv, b = bh / p.Hkv, t = r / p.G, h = hk * p.G + r % p.G;
-    const float2 *ml = p.part_ml + static_cast<size_t>(row) * p.splits;
+    // the row's parts: first index, number, and the step to the next
+    size_t first = static_cast<size_t>(row) * p.splits, step = 1;
+    int parts = p.splits;
+    if (p.share > 0) {
+        int len;
+        const int steps = key_steps(p, b, &len), piece = key_piece(p);
+        parts = (steps + piece - 1) / piece;
+        first = static_cast<size_t>(first_piece(p, b, hk, piece, steps)) * rows + r;
+        step = rows;
+    }
+    const float2 *ml = p.part_ml + first;
     float M = -INFINITY;
-    for (int s = lane; s < p.splits; s += 32) {
-        const float2 x = __ldcg(ml + s);
+    for (int s = lane; s < parts; s += 32) {
+        const float2 x = __ldcg(ml + s * step);
         if (x.y != 0.0f) M = fmaxf(M, x.x);
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
     const int e0 = 8 * lane;
-    const float *po = p.part_o + static_cast<size_t>(row) * p.splits * p.D;
+    const float *po = p.part_o + first * p.D + e0;
     float l = 0.0f, o[8] = {};
-    for (int s = 0; s < p.splits; ++s) {
-        const float2 x = __ldcg(ml + s);
-        if (x.y == 0.0f) continue;
-        const float f = exp2f(x.x - M);
-        l = fmaf(f, x.y, l);
-        if (e0 < p.D) {
-            const float4 a = __ldcg(reinterpret_cast<const float4 *>(po + static_cast<size_t>(s) * p.D + e0));
-            const float4 c = __ldcg(reinterpret_cast<const float4 *>(po + static_cast<size_t>(s) * p.D + e0 + 4));
-            const float y[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+    for (int s0 = 0; s0 < parts; s0 += 32) {
+        float f = 0.0f;
+        if (s0 + lane < parts) {
+            const float2 x = __ldcg(ml + (s0 + lane) * step);
+            if (x.y != 0.0f) f = exp2f(x.x - M);
+            l = fmaf(f, x.y, l);
+        }
+        const int n = min(32, parts - s0);
+#pragma unroll 4
+        for (int s = 0; s < n; ++s) {
+            const float fs = __shfl_sync(0xffffffffu, f, s);
+            if (e0 < p.D && fs != 0.0f) {  // a part without keys may hold anything
+                const float *q = po + (s0 + s) * step * p.D;
+                const float4 a = __ldcg(reinterpret_cast<const float4 *>(q));
+                const float4 c = __ldcg(reinterpret_cast<const float4 *>(q + 4));
+                const float y[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = fmaf(f, y[i], o[i]);
+                for (int i = 0; i < 8; ++i) o[i] = fmaf(fs, y[i], o[i]);
+            }
         }
     }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
     if (e0 >= p.D) return;
     const float f = l != 0.0f ? (p.cached ? p.cache.v.g : 1.0f) / l : 0.0f;
     uint32_t w[4];

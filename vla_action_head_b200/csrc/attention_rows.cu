@@ -20,14 +20,16 @@
 // No barrier of the CTA in the loop, a few instructions a step for the loads.  (8 sequences of 32701
 // cached keys, 256-wide heads: 71 us with loads into registers, 46 with cp.async by every thread, XX.)
 //
-// The warps of a CTA are joined through shared memory; one CTA takes a range of keys, and the ranges
-// of a long sequence are joined by attention_join_kernel.
+// The warps of a CTA are joined through shared memory.  A CTA takes a whole key head, or (long keys,
+// few heads) a piece of one, dealt out by the sequences' lengths (attention_share.cuh); the pieces are
+// joined by attention_join_kernel.
 // The reference m of a row is replaced only when a score outgrows it by 2^8, found by one vote a
 // step, so the steps carry no reductions; l stays per thread until the end.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "attention.h"
+#include "attention_share.cuh"
 #include "gemm.h"
 #include "kv_decode.cuh"
 #include "quant.cuh"
@@ -128,12 +130,11 @@ __device__ __forceinline__ uint32_t swizzled(int r, int c) {
     else return r * 32 + ((c ^ ((r >> 2) & 1)) << 4);
 }
 
-// N elements (from e) of row r of a stage's codes -> fp16 pairs; `on` = 0: zeros whatever the bytes are.
+// N elements (from e) of row r of a stage: their codes and scale bytes (zeros past D).
 template <int DP, bool FULL, int N>
-__device__ __forceinline__ void codes_f16(uint32_t codes, uint32_t sf, int r, int e, int D, bool on,
-                                          uint32_t (&h)[N / 2]) {
-    uint32_t w[N / 8];
-    uint32_t s = 0u;  // scale bytes; zero times any code is zero
+__device__ __forceinline__ void load_codes(uint32_t codes, uint32_t sf, int r, int e, int D, uint32_t (&w)[N / 8],
+                                           uint32_t &s) {
+    s = 0u;
     if constexpr (FULL) {
         const uint32_t a = codes + swizzled<DP / 2>(r, e >> 5) + ((e >> 1) & 15);
         if constexpr (N == 32) {
@@ -168,14 +169,47 @@ __device__ __forceinline__ void codes_f16(uint32_t codes, uint32_t sf, int r, in
             }
         }
     }
-    uint32_t sc[2];
-    scale2_f16x2(on ? s : 0u, sc[0], sc[1]);
+}
+// The same -> fp16 pairs of adjacent elements.
+template <int DP, bool FULL, int N>
+__device__ __forceinline__ void codes_f16(uint32_t codes, uint32_t sf, int r, int e, int D, uint32_t (&h)[N / 2]) {
+    uint32_t w[N / 8], s, sc[2];
+    load_codes<DP, FULL, N>(codes, sf, r, e, D, w, s);
+    scale2_f16x2(s, sc[0], sc[1]);
 #pragma unroll
     for (int q = 0; q < N / 8; ++q) {
         uint32_t d[4];
         decode_e2m1x8_f16(w[q], d);
 #pragma unroll
         for (int k = 0; k < 4; ++k) h[4 * q + k] = mul_f16x2(d[k], sc[q >> 1]);
+    }
+}
+// N elements (from e) of rows r and r + 1 of a stage's codes -> fp16 pairs (row r, row r + 1): lo[i] of
+// element 2i, hi[i] of 2i + 1, the matrix operand as it is.  The codes are paired by nibbles before they
+// are decoded, which is half the work of transposing decoded pairs.  `on`, `on1`: as above.
+template <int DP, bool FULL, int N>
+__device__ __forceinline__ void codes_f16_rows(uint32_t codes, uint32_t sf, int r, int e, int D, bool on, bool on1,
+                                               uint32_t (&lo)[N / 2], uint32_t (&hi)[N / 2]) {
+    uint32_t w[2][N / 8], s[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        load_codes<DP, FULL, N>(codes, sf, r + x, e, D, w[x], s[x]);
+        if (!(x == 0 ? on : on1)) s[x] = 0u;
+    }
+    const uint32_t ss = __byte_perm(s[0], s[1], 0x5140);  // scale bytes of block 0 of both rows, then of block 1
+    uint32_t sc[2];
+    sc[0] = scales_f16x2(ss);
+    sc[1] = N > 16 ? scales_f16x2(ss >> 16) : 0u;
+#pragma unroll
+    for (int q = 0; q < N / 8; ++q) {
+        const uint32_t a = w[0][q], b = w[1][q];
+        uint32_t d[4];
+        decode_e2m1x8_f16((a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u), d);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) lo[4 * q + k] = mul_f16x2(d[k], sc[q >> 1]);
+        decode_e2m1x8_f16(((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u), d);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) hi[4 * q + k] = mul_f16x2(d[k], sc[q >> 1]);
     }
 }
 // 8 elements: 16-byte unit c of row r of a 64-element block.
@@ -206,13 +240,16 @@ __global__ void __launch_bounds__(Cfg<DP, FULL, CACHED>::kThreads, 1)
     __syncwarp();
     pdl_launch_dependents();
     pdl_wait();
-    int rest = static_cast<int>(blockIdx.x);
-    const int split = rest % p.splits;
-    rest /= p.splits;
-    const int hk = rest % p.Hkv, b = rest / p.Hkv;
     const int rows = p.T * p.G;  // <= kRows
-    int len = p.S;
-    if (p.kv_len != nullptr) len = min(max(__ldcg(p.kv_len + b), 0), p.S);
+    const uint32_t sq = smem_u32(smem), ring = sq + C::kQ + warp * C::kStages * C::kStage;
+    const int kc = (p.D + 63) >> 6;
+    const uint64_t policy = policy_evict_first();
+    int slot = 0;
+    uint32_t phase = 0u;
+
+    KeyRange range;
+    if (!key_range(p, range)) return;  // the whole CTA
+    const int b = range.b, hk = range.hk, len = range.len, step0 = range.step0, step1 = range.step1;
 
     // Q (warp 0): row g, the thread's elements of each block of K
     constexpr int kQUnits = DP / 32;  // 8 elements each
@@ -229,14 +266,8 @@ __global__ void __launch_bounds__(Cfg<DP, FULL, CACHED>::kThreads, 1)
         }
     }
 
-    // whole steps of 16 keys to the splits, in turn to the warps
-    const int steps = (len + 15) >> 4, per = (steps + p.splits - 1) / p.splits;
-    const int step0 = split * per, step1 = min(steps, step0 + per);
     const uint8_t *mask = p.mask != nullptr ? p.mask + b * p.mask_stride : nullptr;
     const size_t plane = (static_cast<size_t>(b) * p.Hkv + hk) * p.cache.C;
-    const uint32_t sq = smem_u32(smem), ring = sq + C::kQ + warp * C::kStages * C::kStage;
-    const int kc = (p.D + 63) >> 6;
-    const uint64_t policy = policy_evict_first();
     auto ask = [&](int st, int slot) {  // lane 0
         const uint32_t to = ring + slot * C::kStage, on = bar + 8 * slot;
         if constexpr (CACHED) {
@@ -262,8 +293,10 @@ __global__ void __launch_bounds__(Cfg<DP, FULL, CACHED>::kThreads, 1)
         }
     };
     if (lane == 0)
-        for (int i = 0; i < C::kStages; ++i)
-            if (step0 + warp + i * kWarps < step1) ask(step0 + warp + i * kWarps, i);
+        for (int i = 0, to = slot; i < C::kStages; ++i) {
+            if (step0 + warp + i * kWarps < step1) ask(step0 + warp + i * kWarps, to);
+            to = to + 1 == C::kStages ? 0 : to + 1;
+        }
     // lane's key of a step, 1 if it is attended to; asked for one step ahead
     auto key_on = [&](int st) -> uint32_t {
         const int j = 16 * st + (lane & 15);
@@ -304,8 +337,6 @@ __global__ void __launch_bounds__(Cfg<DP, FULL, CACHED>::kThreads, 1)
 
     float o[kTiles][4] = {};
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};  // rows 2t, 2t + 1; m in units of log2
-    int slot = 0;
-    uint32_t phase = 0u;
     for (int st = step0 + warp; st < step1; st += kWarps) {
         const uint32_t keys = __ballot_sync(0xffffffffu, key != 0u);
         key = key_on(st + kWarps);
@@ -329,8 +360,8 @@ __global__ void __launch_bounds__(Cfg<DP, FULL, CACHED>::kThreads, 1)
         for (int i = 0; i < C::kKBlocks; ++i) {
             uint32_t h0[C::kKBlock / 2], h1[C::kKBlock / 2];
             if constexpr (CACHED) {
-                codes_f16<DP, FULL, C::kKBlock>(at, at + C::kOffKs, g, C::k_element(t, i), p.D, true, h0);
-                codes_f16<DP, FULL, C::kKBlock>(at, at + C::kOffKs, g + 8, C::k_element(t, i), p.D, true, h1);
+                codes_f16<DP, FULL, C::kKBlock>(at, at + C::kOffKs, g, C::k_element(t, i), p.D, h0);
+                codes_f16<DP, FULL, C::kKBlock>(at, at + C::kOffKs, g + 8, C::k_element(t, i), p.D, h1);
             } else {
                 wide_pairs(at + (i >> 1) * 2048, g, 2 * t + (i & 1), true, h0);
                 wide_pairs(at + (i >> 1) * 2048, g + 8, 2 * t + (i & 1), true, h1);
@@ -375,24 +406,33 @@ __global__ void __launch_bounds__(Cfg<DP, FULL, CACHED>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
             pb[i] = transpose8x8(CACHED ? pack_f16x2(w[2 * i], w[2 * i + 1]) : pack_bf16x2_rn(w[2 * i], w[2 * i + 1]));
-        // keys 2t, 2t + 1, 2t + 8, 2t + 9; zeros for the left-out ones
+        // keys 2t, 2t + 1, 2t + 8, 2t + 9; zeros for the left-out ones (whatever their bytes are)
 #pragma unroll
         for (int i = 0; i < C::kVBlocks; ++i) {
-            uint32_t h[4][C::kVBlock / 2];
+            // pairs of keys (2t, 2t + 1) and (2t + 8, 2t + 9): element 2x in lo[x], 2x + 1 in hi[x]
+            uint32_t lo[2][C::kVBlock / 2], hi[2][C::kVBlock / 2];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int j = 2 * t + (k & 1) + 8 * (k >> 1);
-                const bool on = ((keys >> j) & 1u) != 0u;
-                if constexpr (CACHED)
-                    codes_f16<DP, FULL, C::kVBlock>(vat, at + C::kOffVs, j, C::v_element(g, i), p.D, on, h[k]);
-                else
-                    wide_pairs(vat + i * 2048, j, g, on, h[k]);
+            for (int k = 0; k < 2; ++k) {
+                const int j = 2 * t + 8 * k;
+                const bool on = ((keys >> j) & 1u) != 0u, on1 = ((keys >> (j + 1)) & 1u) != 0u;
+                if constexpr (CACHED) {
+                    codes_f16_rows<DP, FULL, C::kVBlock>(vat, at + C::kOffVs, j, C::v_element(g, i), p.D, on, on1, lo[k],
+                                                         hi[k]);
+                } else {
+                    uint32_t h0[4], h1[4];
+                    wide_pairs(vat + i * 2048, j, g, on, h0);
+                    wide_pairs(vat + i * 2048, j + 1, g, on1, h1);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        lo[k][x] = __byte_perm(h0[x], h1[x], 0x5410);
+                        hi[k][x] = __byte_perm(h0[x], h1[x], 0x7632);
+                    }
+                }
             }
 #pragma unroll
-            for (int k = 0; k < C::kVBlock / 2; ++k) {  // pair (e, e + 1): rows g and g + 8 of a tile
-                const uint32_t a[4] = {__byte_perm(h[0][k], h[1][k], 0x5410), __byte_perm(h[0][k], h[1][k], 0x7632),
-                                       __byte_perm(h[2][k], h[3][k], 0x5410), __byte_perm(h[2][k], h[3][k], 0x7632)};
-                mma16816<CACHED>(o[i * (C::kVBlock / 2) + k], a, pb[0], pb[1]);
+            for (int x = 0; x < C::kVBlock / 2; ++x) {  // rows g and g + 8 of a tile: elements 2x and 2x + 1
+                const uint32_t a[4] = {lo[0][x], hi[0][x], lo[1][x], hi[1][x]};
+                mma16816<CACHED>(o[i * (C::kVBlock / 2) + x], a, pb[0], pb[1]);
             }
         }
         __syncwarp();  // every lane has read the stage
@@ -419,28 +459,38 @@ __global__ void __launch_bounds__(Cfg<DP, FULL, CACHED>::kThreads, 1)
                 make_float2(o[j][i], o[j][2 + i]);
     }
     __syncthreads();
+    // each warp's factor against the row's largest reference, and the row's sum
+    for (int r = warp; r < rows; r += kWarps) {
+        const float lw = lane < kWarps ? sm_l[lane][r] : 0.0f, mw = lane < kWarps && lw != 0.0f ? sm_m[lane][r] : -INFINITY;
+        float M = mw;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+        const float f = lw != 0.0f ? ex2(sm_m[lane][r] - M) : 0.0f;
+        float sum = f * lw;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (lane < kWarps) sm_l[lane][r] = f;
+        if (lane == 0) sm_q[r] = sum;
+        if (lane == 0 && p.share > 0) p.part_ml[static_cast<size_t>(blockIdx.x) * rows + r] = make_float2(M, sum);
+    }
+    __syncthreads();
     // a thread: every kThreads-th pair of elements of the rows
     for (int x = threadIdx.x; x < rows * (DP / 2); x += kThreads) {
         const int r = x / (DP / 2), pair = x % (DP / 2), e = C::o_element(pair & 7, pair >> 3);
-        float M = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w)
-            if (sm_l[w][r] != 0.0f) M = fmaxf(M, sm_m[w][r]);
-        float sum = 0.0f, a0 = 0.0f, a1 = 0.0f;
+        if (e >= p.D) continue;
+        float a0 = 0.0f, a1 = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            if (sm_l[w][r] == 0.0f) continue;
-            const float f = ex2(sm_m[w][r] - M);
+            // (a warp without keys has a factor of 0, and sums of 0)
+            const float f = sm_l[w][r];
             const float2 v = *reinterpret_cast<const float2 *>(smem_o + (w * kRows + r) * C::kPitch + 2 * pair);
-            sum = fmaf(f, sm_l[w][r], sum);
             a0 = fmaf(f, v.x, a0);
             a1 = fmaf(f, v.y, a1);
         }
-        if (p.splits > 1) {
-            const size_t at = ((static_cast<size_t>(b) * p.Hkv + hk) * rows + r) * p.splits + split;
-            if (pair == 0) p.part_ml[at] = make_float2(M, sum);
-            if (sum != 0.0f && e < p.D) *reinterpret_cast<float2 *>(p.part_o + at * p.D + e) = make_float2(a0, a1);
-        } else if (e < p.D) {
+        const float sum = sm_q[r];
+        if (p.share > 0) {
+            *reinterpret_cast<float2 *>(p.part_o + (static_cast<size_t>(blockIdx.x) * rows + r) * p.D + e) = make_float2(a0, a1);
+        } else {
             const float f = sum != 0.0f ? (CACHED ? p.cache.v.g : 1.0f) / sum : 0.0f;
             const int tq = r / p.G, hq = hk * p.G + r - tq * p.G;
             *reinterpret_cast<uint32_t *>(p.out.ptr + b * p.out.sb + tq * p.out.st + hq * p.out.sh + e) =
@@ -456,7 +506,7 @@ cudaError_t launch_rows(const CUtensorMap &mk, const CUtensorMap &mv, const Attn
     using C = Cfg<DP, FULL, CACHED>;
     cudaError_t e = set_smem_limit_once(reinterpret_cast<const void *>(kernel), C::kSmem, attr_set);
     if (e != cudaSuccess) return e;
-    const long long ctas = static_cast<long long>(a.B) * a.Hkv * a.splits;
+    const long long ctas = a.share > 0 ? a.share : static_cast<long long>(a.B) * a.Hkv;
     if (ctas > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas));
@@ -483,6 +533,8 @@ bool attention_rows_mapped(const AttnArgs &a) {
     return (a.D == 64 || a.D == 128 || a.D == 256) &&
            static_cast<long long>(a.B) * a.Hkv * a.cache.C < 0x7FFFFFFFLL;
 }
+
+int attention_rows_warps(bool cached, int D) { return cached ? 16 : D > 128 ? 4 : 8; }
 
 cudaError_t launch_attention_rows(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a, cudaStream_t s) {
     if (a.D <= 64) return launch_rows_dp<64>(mk, mv, a, s);

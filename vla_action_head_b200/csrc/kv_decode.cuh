@@ -49,14 +49,18 @@ __device__ __forceinline__ uint32_t scale_f16x2(uint32_t byte) {
     return r;
 }
 
-// Two scale bytes (the low 16 bits) -> two fp16 pairs (s0, s0) and (s1, s1), exact.
-__device__ __forceinline__ void scale2_f16x2(uint32_t bytes, uint32_t &s0, uint32_t &s1) {
+// Two scale bytes (the low 16 bits) -> the fp16 pair (s0, s1), or (s0, s0) and (s1, s1); exact.
+__device__ __forceinline__ uint32_t scales_f16x2(uint32_t bytes) {
     uint32_t r;
     asm("{\n\t.reg .b16 h;\n\t"
         "cvt.u16.u32 h, %1;\n\t"
         "cvt.rn.f16x2.e4m3x2 %0, h;\n\t}"
         : "=r"(r)
         : "r"(bytes));
+    return r;
+}
+__device__ __forceinline__ void scale2_f16x2(uint32_t bytes, uint32_t &s0, uint32_t &s1) {
+    const uint32_t r = scales_f16x2(bytes);
     s0 = __byte_perm(r, r, 0x1010);
     s1 = __byte_perm(r, r, 0x3232);
 }
