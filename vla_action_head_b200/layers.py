@@ -19,10 +19,17 @@ epilogues into preallocated buffers, so a forward can be captured in a CUDA grap
   PrefillLayer       backbone-shaped prefill layer at M = 968: RMSNorm->FP4, QKV,
                      RMSNorm->FP4, gate/up GeGLU -> FP4, down (+residual).
 
-Attention itself is not part of the linear path: the attention-output GEMM reads a
-caller-supplied bf16 context tensor (quantized with the plain quantizer), which stands in
-for the attention result.
+The attention-output GEMM reads a bf16 context tensor (quantized with the plain quantizer).
+A caller may supply it, standing in for the attention result, or pass None: the layer then
+attends itself, between its QKV and its attention-output GEMM:
+
+  PrefillLayer        with `attend`: turns its keys and writes keys and values into the cache
+  ActionExpertLayer,  turn queries and keys, append keys and values to the cache and attend to
+  GatedAction...      its rows (the prompt's and their own), all tokens to all (no causal order)
+  DiTLayer            attends to the keys and values of an encoder, or to its own tokens
 """
+from dataclasses import dataclass
+
 import torch
 
 from . import nvfp4, synth
@@ -45,8 +52,42 @@ def _rand(seed, shape, mean, std, device):
     return synth.bf16_normal_torch(seed, shape, mean, std, device=device)
 
 
+@dataclass
+class Attend:
+    """What a layer with a key/value cache attends with.  cache: one sequence's NVFP4 cache of this
+    layer; start: int32 [1], the cache row (and position) of the call's first token; table:
+    nvfp4.rope_table; kv_len: int32 [1], the keys after the call's rows are written (not needed to
+    fill the cache)."""
+    cache: nvfp4.KVCache
+    start: torch.Tensor
+    table: torch.Tensor
+    kv_len: torch.Tensor = None
+
+
+class _CacheAttention:
+    """The step between QKV output [M, (Hq + 2 Hkv) D] and context of the layers with a cache."""
+
+    def __init__(self, M, Hq, Hkv, D, device):
+        self.M, self.Hq, self.Hkv, self.D = M, Hq, Hkv, D
+        self.q = torch.empty((1, M, Hq, D), dtype=torch.bfloat16, device=device)
+        self.context = torch.empty((1, M, Hq, D), dtype=torch.bfloat16, device=device)
+        self.ws = nvfp4.Workspace(device)
+
+    def store(self, qkv, attend):
+        """Turns keys, and queries into self.q; keys and values into the cache."""
+        qkv = qkv.view(1, self.M, self.Hq + 2 * self.Hkv, self.D)
+        q, k, v = qkv.split([self.Hq, self.Hkv, self.Hkv], 2)
+        nvfp4.qk_norm_rope(q, k, table=attend.table, norm=False, v=v, cache=attend.cache, start=attend.start,
+                           q_out=self.q)
+
+    def __call__(self, qkv, attend):
+        self.store(qkv, attend)
+        nvfp4.attention(self.q, cache=attend.cache, kv_len=attend.kv_len, out=self.context, workspace=self.ws)
+        return self.context.view(self.M, self.Hq * self.D)
+
+
 class DiTLayer:
-    def __init__(self, M=41, H=1536, F=6144, wl=2, layer=0, device="cuda", ws=None):
+    def __init__(self, M=41, H=1536, F=6144, wl=2, layer=0, device="cuda", ws=None, heads=32):
         s = lambda tid: synth.seed_of(wl, 100 * layer + tid)  # noqa: E731
         d = device
         self.M, self.H, self.F = M, H, F
@@ -66,14 +107,28 @@ class DiTLayer:
         self.u = nvfp4.empty_fp4(M, F, d)
         self.qkv_out = torch.empty((M, 3 * H), dtype=torch.bfloat16, device=d)
         self.h = torch.empty((M, H), dtype=torch.bfloat16, device=d)
+        self.heads = heads
+        self.context = torch.empty((1, M, heads, H // heads), dtype=torch.bfloat16, device=d)
+        self.attend_ws = nvfp4.Workspace(d)
 
     def linears(self):
         return [self.qkv, self.o, self.up, self.down]
 
-    def forward(self, x, context, y):
-        """x, context: bf16 [M, H]; writes the layer output into y (bf16 [M, H])."""
+    def attend(self, encoder=None, key_mask=None):
+        """Context of the layer's queries over encoder = (k, v), bf16 [1, S, heads, H / heads] views
+        (key_mask bool [1, S]), or, without, over its own tokens; from the QKV output."""
+        q, k, v = self.qkv_out.view(1, self.M, 3 * self.heads, -1).split(self.heads, 2)
+        k, v = (k, v) if encoder is None else encoder
+        nvfp4.attention(q, k, v, key_mask=key_mask, out=self.context, workspace=self.attend_ws)
+        return self.context.view(self.M, self.H)
+
+    def forward(self, x, context, y, encoder=None, key_mask=None):
+        """x, context: bf16 [M, H]; writes the layer output into y (bf16 [M, H]).  context None: the
+        layer attends itself (see attend)."""
         nvfp4.quantize_norm(x, "adaln", scale=self.ada_scale, shift=self.ada_shift, eps=1e-6, out=self.a1)
         nvfp4.gemm(self.a1, self.qkv.w, "bias", bias=self.qkv.bias, out=self.qkv_out, workspace=self.ws)
+        if context is None:
+            context = self.attend(encoder, key_mask)
         nvfp4.quantize_norm(context, "none", out=self.ctx_q)
         nvfp4.gemm(self.ctx_q, self.o.w, "bias_residual", bias=self.o.bias, residual=x, out=self.h, workspace=self.ws)
         nvfp4.quantize_norm(self.h, "layernorm", gamma=self.ln_gamma, beta=self.ln_beta, eps=1e-5, out=self.a2)
@@ -82,7 +137,7 @@ class DiTLayer:
                    workspace=self.ws)
         return y
 
-    launches = 7
+    launches = 7  # with a context of the caller's; attending itself, its own launches come on top
 
 
 class ActionExpertLayer:
@@ -106,14 +161,18 @@ class ActionExpertLayer:
         self.u = nvfp4.empty_fp4(M, F, d)
         self.qkv_out = torch.empty((M, 2560), dtype=torch.bfloat16, device=d)
         self.h = torch.empty((M, H), dtype=torch.bfloat16, device=d)
+        self.attention = _CacheAttention(M, A // 256, 1, 256, d)
 
     def linears(self):
         return [self.qkv, self.o, self.gate_up, self.down]
 
-    def forward(self, x, context, y):
-        """x: bf16 [M, H]; context: bf16 [M, A]; writes the output into y (bf16 [M, H])."""
+    def forward(self, x, context, y, attend=None):
+        """x: bf16 [M, H]; context: bf16 [M, A], or None with `attend` (Attend): the layer's tokens are
+        appended to the cache and attend to it; writes the output into y (bf16 [M, H])."""
         nvfp4.quantize_norm(x, "adarms", scale=self.scale1, eps=1e-6, out=self.a1)
         nvfp4.gemm(self.a1, self.qkv.w, "none", out=self.qkv_out, workspace=self.ws)
+        if context is None:
+            context = self.attention(self.qkv_out, attend)
         nvfp4.quantize_norm(context, "none", out=self.ctx_q)
         nvfp4.gemm(self.ctx_q, self.o.w, "residual", residual=x, out=self.h, workspace=self.ws)
         nvfp4.quantize_norm(self.h, "adarms", scale=self.scale2, eps=1e-6, out=self.a2)
@@ -159,21 +218,25 @@ class GatedActionExpertLayer:
         self.a2 = nvfp4.empty_fp4(M, H, d)
         self.u = nvfp4.empty_fp4(M, F, d)
         self.qkv_out = torch.empty((M, 2560), dtype=torch.bfloat16, device=d)
+        self.attention = _CacheAttention(M, A // 256, 1, 256, d)
         self.d_o = torch.empty((M, H), dtype=torch.bfloat16, device=d)
         self.d_out = torch.empty((M, H), dtype=torch.bfloat16, device=d)
 
     def linears(self):
         return [self.qkv, self.o, self.gate_up, self.down]
 
-    def forward(self, r, d_in, g_in, context):
+    def forward(self, r, d_in, g_in, context, attend=None):
         """r: bf16 [M, H] residual stream (updated in place); d_in, g_in: the previous layer's
-        down output and gate (d_in None: a plain AdaRMS front-end for the first layer)."""
+        down output and gate (d_in None: a plain AdaRMS front-end for the first layer); context:
+        bf16 [M, A], or None with `attend` (Attend), as for ActionExpertLayer."""
         if d_in is None:
             nvfp4.quantize_norm(r, "adarms", scale=self.s1, shift=self.t1, eps=1e-6, out=self.a1)
         else:
             nvfp4.residual_quantize_norm(r, d_in, g_in, "adarms", scale=self.s1, shift=self.t1, eps=1e-6,
                                          h_out=r, out=self.a1)
         nvfp4.gemm(self.a1, self.qkv.w, "none", out=self.qkv_out, workspace=self.ws)
+        if context is None:
+            context = self.attention(self.qkv_out, attend)
         nvfp4.quantize_norm(context, "none", out=self.ctx_q)
         nvfp4.gemm(self.ctx_q, self.o.w, "none", out=self.d_o, workspace=self.ws)
         nvfp4.residual_quantize_norm(r, self.d_o, self.g1, "adarms", scale=self.s2, shift=self.t2, eps=1e-6,
@@ -200,13 +263,18 @@ class PrefillLayer:
         self.a2 = nvfp4.empty_fp4(M, H, d)
         self.u = nvfp4.empty_fp4(M, F, d)
         self.qkv_out = torch.empty((M, 2560), dtype=torch.bfloat16, device=d)
+        self.attention = _CacheAttention(M, 8, 1, 256, d)
 
     def linears(self):
         return [self.qkv, self.gate_up, self.down]
 
-    def forward(self, x, context, y):
+    def forward(self, x, context, y, attend=None):
+        """x: bf16 [M, H]; writes the output into y (bf16 [M, H]).  attend (Attend): the tokens' keys and
+        values are written into its cache (context is not used: the layer has no attention-output GEMM)."""
         nvfp4.quantize_norm(x, "rmsnorm", gamma=self.gamma1, eps=1e-6, out=self.a1)
         nvfp4.gemm(self.a1, self.qkv.w, "none", out=self.qkv_out, workspace=self.ws)
+        if attend is not None:
+            self.attention.store(self.qkv_out, attend)
         nvfp4.quantize_norm(x, "rmsnorm", gamma=self.gamma2, eps=1e-6, out=self.a2)
         nvfp4.gemm(self.a2, self.gate_up.w, "geglu", out=self.u, workspace=self.ws)
         nvfp4.gemm(self.u, self.down.w, "residual", residual=x, out=y, workspace=self.ws)
