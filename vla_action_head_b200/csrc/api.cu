@@ -511,8 +511,8 @@ bool attention_few_rows(const AttnArgs &a) { return static_cast<long long>(a.T) 
 
 // Tile kernel: parts of the key range, the number of least modelled time (us).
 int attention_splits(const AttnArgs &a) {
-    const int slots = sm_count_cached() * (!a.cached && a.D <= 128 ? 2 : 1);
-    const long long tiles = (static_cast<long long>(a.T) * a.G + 127) / 128 * a.B * a.Hkv;
+    const int slots = sm_count_cached(), rows = !a.cached && a.D <= 128 ? 256 : 128;  // a CTA's
+    const long long tiles = (static_cast<long long>(a.T) * a.G + rows - 1) / rows * a.B * a.Hkv;
     const int keys = (a.S + 127) / 128;
     int best = 1;
     double best_cost = 1e300;

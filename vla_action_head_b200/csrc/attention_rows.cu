@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(Cfg<DP, FULL, CACHED>::kThreads, 1)
     uint32_t key = key_on(step0 + warp);
 
     if (warp == 0) {  // Q as the operand words of each step of 16 elements
-        float up = 1.0f;
+        float up = 1.0f, down = 1.0f;
         if constexpr (CACHED) {
             float top = 0.0f;
 #pragma unroll
@@ -317,9 +317,9 @@ __global__ void __launch_bounds__(Cfg<DP, FULL, CACHED>::kThreads, 1)
             }
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            up = f16_row_factor(top);
+            up = f16_row_factor(top, &down);
         }
-        if (t == 0) sm_q[g] = 1.0f / up;
+        if (t == 0) sm_q[g] = down;
 #pragma unroll
         for (int i = 0; i < kQUnits; ++i) {
             uint32_t w[4] = {qu[i].x, qu[i].y, qu[i].z, qu[i].w};

@@ -4,21 +4,24 @@
 //   l = sum p;  O += P V;  out = O / l,                  c = scale log2(e)
 //
 // The rows of a tile are the (query, head) pairs that share a key head, query-major, so a group of
-// G heads reads its keys once.  One CTA takes one row tile and a range of key tiles (the whole
-// sequence, or one of `splits` parts whose O, m and l are joined by attention_join_kernel).
+// G heads reads its keys once.  One CTA takes one row tile (cache, or heads wider than 128) or two, and a
+// range of key tiles (the whole sequence, or one of `splits` parts whose O, m and l are joined by
+// attention_join_kernel).
 //
-// Roles (192 threads; cache: 384): warp 5 brings K and V through a ring of 16 KB chunks by TMA (a K chunk is 128
-// keys x 64 elements, a V chunk all elements of 16384 / (2 DP) keys: both are what one step of
-// the MMA loop eats), warp 4 issues the MMAs, warps 0-3 own a row a thread: scores from tensor
-// memory, softmax, P back to tensor memory as the A operand of P V, where it overwrites its own
-// scores.  With 256-wide heads O takes half of the tensor memory and two score tiles the rest, so
-// Q K^T of the next tile runs under the softmax of this one; narrower heads keep one score tile
-// and half of the tensor and shared memory, and two CTAs share an SM and fill each other's gaps.
+// Roles: eight warps per row tile own half a row a thread (64 keys; the halves exchange their maxima):
+// scores from tensor memory, softmax, P back to tensor memory as the A operand of P V, where it
+// overwrites scores.  The next warp issues the MMAs, the last brings K and V through a ring of 16 KB
+// chunks by TMA (a K chunk is 128 keys x 64 elements, a V chunk all elements of 16384 / (2 DP) keys: both
+// are what one step of the MMA loop eats).  Tensor memory holds the row tiles' O (256 columns) and two
+// score tiles.  Two row tiles read each chunk of K and V once, and one's products run under the other's
+// softmax.  One row tile uses the score tiles in turn: Q K^T of the next keys runs under the softmax of these.
+// (A row a thread was 2.6 us of softmax a tile against 1 us of products; two CTAs per SM with one row tile
+// each instead of one CTA with two: XX against YY us for 8 x 2048 queries over 4096 keys of 128.)
 //
 // O is rescaled only where the row maximum outgrew the reference by more than 2^8 (the weights
 // stay below 2^8, l and O are fp32; the final division cancels the reference).
 //
-// Cache: warps 5-11 take TMA's place: they load codes and scales, several pieces ahead, and write
+// Cache: seven warps take TMA's place: they load codes and scales, several pieces ahead, and write
 // fp16 (code times scale is exact there) into the same ring; queries and weights are fp16 too.
 //
 // Left-out keys: their scores become -inf whatever they hold, and their V rows are zeroed in
@@ -43,27 +46,27 @@ constexpr int kAhead = 4;      // cache: loads of a dequantizing warp on their w
 
 template <int DP, bool CACHED>
 struct Cfg {
-    static constexpr bool kBig = CACHED || DP == 256;        // one CTA per SM, two score tiles
-    static constexpr int kThreads = CACHED ? 32 * (5 + kDequant) : 192;
-    static constexpr int kScores = kBig ? 2 : 1;             // score tiles in tensor memory
-    static constexpr int kRing = kBig ? 10 : 5;              // chunks
-    static constexpr int kVC = DP / 64;                      // V chunks of a tile
+    static constexpr int kTiles = !CACHED && DP <= 128 ? 2 : 1;  // row tiles of a CTA
+    static constexpr int kSoftmax = 8 * kTiles;              // warps; then the MMA warp, then the producers
+    static constexpr int kThreads = 32 * (kSoftmax + 1 + (CACHED ? kDequant : 1));
+    static constexpr int kVC = DP / 64;                      // V chunks of a key tile
     static constexpr int kKeysPerV = 128 / kVC;              // keys of a V chunk
-    static constexpr int kQBytes = 128 * DP * 2;
-    static constexpr int kOffRing = kQBytes;
+    static constexpr int kRing = kTiles == 2 && DP == 128 ? 9 : 10;  // chunks
+    static constexpr int kQTile = 128 * DP * 2;
+    static constexpr int kOffRing = kTiles * kQTile;
     static constexpr int kOffBar = kOffRing + kRing * kChunk;
-    // full[kRing], empty[kRing], s_full[2], p_ready[2], o_done, all_done, q_ready
+    // full[kRing], empty[kRing], s_full[2], p_ready[2], o_done[2], all_done, q_ready
     static constexpr int kOffMisc = kOffBar + (2 * kRing + 8) * 8;
-    static constexpr int kOffRow = kOffMisc + 16;            // cache: a score factor per row
+    static constexpr int kOffMax = kOffMisc + 16;            // exchanged: [parity][half][row]
+    static constexpr int kOffRow = kOffMax + kTiles * 2048;  // cache: a score factor per row
     static constexpr int kSmem = kOffRow + (CACHED ? 512 : 0);
-    static constexpr int kTmemCols = kBig ? 512 : 256;
-    static constexpr int kColS = kBig ? 256 : 128;           // O at 0, then the score tiles
-    static constexpr int kCtas = kBig ? 1 : 2;               // per SM
-    static constexpr bool kKeep = DP == 256 && !CACHED;      // a softmax thread has registers for its 128 scores
+    // O of the row tiles (128 or 256 columns in all), then two score tiles
+    static constexpr int kTmemCols = 512, kColS = 256;
+    // a row on its way out, padded so that the rows of a warp's lanes lie on different banks
+    static constexpr int kOutPitch = DP * 4 + 16;
+    static_assert(kTiles * 128 * kOutPitch <= kRing * kChunk, "staging of the output rows in the ring");
+    static_assert(kSmem <= 232448, "shared memory");
 };
-static_assert(Cfg<256, false>::kSmem <= 232448 && Cfg<256, true>::kSmem <= 232448 &&
-                  2 * (Cfg<128, false>::kSmem + 1024) <= 233472,
-              "shared memory");
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -71,17 +74,13 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// Ring positions of a tile's first K and V chunk.  The MMA loop's order is K0 K1 V0 K2 V1 ... with
-// two score tiles, K0 V0 K1 V1 ... with one.
-template <int SCORES>
-__device__ __forceinline__ int k_pos(int i, int kc, int vc) {
-    if constexpr (SCORES == 1) return i * (kc + vc);
-    return i == 0 ? 0 : kc + (i - 1) * (kc + vc);
+// Ring positions of a key tile's first K and V chunk.  The MMA loop's order is K0 V0 K1 V1 ... with two
+// row tiles, K0 K1 V0 K2 V1 ... with one (whose two score tiles then take turns).
+__device__ __forceinline__ int k_pos(bool two, int i, int kc, int vc) {
+    return two ? i * (kc + vc) : i == 0 ? 0 : kc + (i - 1) * (kc + vc);
 }
-template <int SCORES>
-__device__ __forceinline__ int v_pos(int i, int n, int kc, int vc) {
-    if constexpr (SCORES == 1) return i * (kc + vc) + kc;
-    return i < n - 1 ? 2 * kc + i * (kc + vc) : n * kc + i * vc;
+__device__ __forceinline__ int v_pos(bool two, int i, int n, int kc, int vc) {
+    return two ? i * (kc + vc) + kc : i < n - 1 ? 2 * kc + i * (kc + vc) : n * kc + i * vc;
 }
 
 // Cache: a dequantizing warp's piece of a chunk is 32 rows (keys) of one 64-element block: per lane
@@ -127,17 +126,19 @@ __device__ __forceinline__ void store_f16(uint8_t *base, int r, const Codes &x) 
 }
 
 template <int DP, bool CACHED>
-__global__ void __launch_bounds__(Cfg<DP, CACHED>::kThreads, Cfg<DP, CACHED>::kCtas)
+__global__ void __launch_bounds__(Cfg<DP, CACHED>::kThreads, 1)
     attention_tiles_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                            const AttnArgs p) {
     using C = Cfg<DP, CACHED>;
     extern __shared__ __align__(1024) uint8_t smem[];  // 128-byte swizzle atoms
     const uint32_t sbase = smem_u32(smem);
     const uint32_t bar_full = sbase + C::kOffBar, bar_empty = bar_full + 8 * C::kRing;
-    const uint32_t bar_s = bar_empty + 8 * C::kRing, bar_p = bar_s + 16, bar_o = bar_p + 16, bar_all = bar_o + 8, bar_q = bar_all + 8;
+    const uint32_t bar_s = bar_empty + 8 * C::kRing, bar_p = bar_s + 16, bar_o = bar_p + 16;
+    const uint32_t bar_all = bar_o + 16, bar_q = bar_all + 8;
     volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(smem + C::kOffMisc);  // TMEM base, abort
     volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 1);
     float *row_factor = reinterpret_cast<float *>(smem + C::kOffRow);
+    float *maxima = reinterpret_cast<float *>(smem + C::kOffMax);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     // the CTA's place: split fastest, then row tile, key head, sequence
@@ -145,9 +146,10 @@ __global__ void __launch_bounds__(Cfg<DP, CACHED>::kThreads, Cfg<DP, CACHED>::kC
     const int split = rest % p.splits;
     rest /= p.splits;
     const int rows = p.T * p.G;
-    const int row_tiles = (rows + 127) >> 7;
-    const int row0 = (rest % row_tiles) << 7;
+    const int row_tiles = (rows + 128 * C::kTiles - 1) / (128 * C::kTiles);
+    const int row0 = (rest % row_tiles) * (128 * C::kTiles);
     rest /= row_tiles;
+    const bool two = C::kTiles == 2 && row0 + 128 < rows;  // both row tiles have rows
     const int hk = rest % p.Hkv, b = rest / p.Hkv;
 
     if (threadIdx.x == 0) {
@@ -157,15 +159,16 @@ __global__ void __launch_bounds__(Cfg<DP, CACHED>::kThreads, Cfg<DP, CACHED>::kC
         }
         mbar_init(bar_s, 1);
         mbar_init(bar_s + 8, 1);
-        mbar_init(bar_p, 128);
-        mbar_init(bar_p + 8, 128);
+        mbar_init(bar_p, 256);
+        mbar_init(bar_p + 8, 256);
         mbar_init(bar_o, 1);
+        mbar_init(bar_o + 8, 1);
         mbar_init(bar_all, 1);
-        mbar_init(bar_q, 128);
+        mbar_init(bar_q, two ? 512 : 256);
         misc[1] = 0;
         fence_mbar_init();
     }
-    if (warp == 4) {
+    if (warp == C::kSoftmax) {
         tmem_alloc(smem_u32(const_cast<uint32_t *>(misc)), C::kTmemCols);
         tmem_relinquish();
     }
@@ -182,7 +185,59 @@ __global__ void __launch_bounds__(Cfg<DP, CACHED>::kThreads, Cfg<DP, CACHED>::kC
     const int kc = (p.D + 63) >> 6;  // 64-element blocks of a head
     constexpr int vc = C::kVC;
 
-    if (CACHED && warp >= 5) {
+    if (CACHED && n > 0) {
+        // Q: bf16 -> fp16 by all warps, a row times the power of two that brings its largest element to
+        // [2^14, 2^15) (what falls below fp16's range is 2^-39 of that element); the inverse goes into the
+        // row's score factor.  kUnits lanes a row, several rows in flight.
+        constexpr int kUnits = DP / 8, kStep = C::kThreads / kUnits, kBatch = 4;
+        const int c = threadIdx.x % kUnits, r0 = threadIdx.x / kUnits;
+        const uint16_t *base = p.q.ptr + b * p.q.sb + static_cast<long long>(hk) * p.G * p.q.sh + 8 * c;
+        for (int rb = r0; rb < 128; rb += kBatch * kStep) {
+            uint4 v[kBatch];
+            uint32_t top[kBatch];  // magnitudes as bf16 bits, which order as integers
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int row = row0 + rb + i * kStep;
+                v[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (rb + i * kStep < 128 && row < rows && 8 * c < p.D) {
+                    const int t = row / p.G, g = row - t * p.G;
+                    v[i] = __ldcg(reinterpret_cast<const uint4 *>(base + t * p.q.st + g * p.q.sh));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const uint32_t m2 = __vmaxu2(__vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu),
+                                             __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
+                top[i] = max(m2 & 0xFFFFu, m2 >> 16);
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; i += 2) {  // two rows a shuffle
+                uint32_t two = top[i] | (top[i + 1] << 16);
+#pragma unroll
+                for (int d = kUnits / 2; d > 0; d >>= 1) two = __vmaxu2(two, __shfl_xor_sync(0xffffffffu, two, d));
+                top[i] = two << 16;
+                top[i + 1] = two & 0xFFFF0000u;
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int r = rb + i * kStep;
+                if (r >= 128) break;
+                float down;
+                const float up = f16_row_factor(__uint_as_float(top[i]), &down);
+                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                uint32_t h[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) h[k] = pack_f16x2(bf16lo(w[k]) * up, bf16hi(w[k]) * up);
+                *reinterpret_cast<uint4 *>(smem + (c >> 3) * kChunk + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
+                    make_uint4(h[0], h[1], h[2], h[3]);
+                if (c == 0) row_factor[r] = down;
+            }
+        }
+        fence_proxy_async_smem();
+        __syncthreads();
+    }
+
+    if (CACHED && warp > C::kSoftmax) {
         // ------------------------------ dequantizers ------------------------------
         // the chunks' pieces in the order of the ring, in turn to the warps
         const uint8_t *mask = p.mask != nullptr ? p.mask + b * p.mask_stride : nullptr;
@@ -221,7 +276,7 @@ __global__ void __launch_bounds__(Cfg<DP, CACHED>::kThreads, Cfg<DP, CACHED>::kC
             return load_codes(f.is_v ? p.cache.v : p.cache.k, plane + j, f.e0, p.D, on);
         };
         Codes q[kAhead];
-        const int x0 = warp - 5;
+        const int x0 = warp - C::kSoftmax - 1;
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) q[i] = fetch(x0 + i * kDequant);
         bool ok = true;
@@ -243,7 +298,7 @@ __global__ void __launch_bounds__(Cfg<DP, CACHED>::kThreads, Cfg<DP, CACHED>::kC
                 }
             }
         }
-    } else if (warp == 5) {
+    } else if (warp > C::kSoftmax) {
         if (elect_one()) {
             // ------------------------------ producer ------------------------------
             const uint64_t pol = policy_evict_last();
@@ -276,260 +331,218 @@ __global__ void __launch_bounds__(Cfg<DP, CACHED>::kThreads, Cfg<DP, CACHED>::kC
             };
             if (n > 0) load_k(0);
             for (int i = 0; i < n && ok; ++i) {
-                if (C::kScores == 2 && i + 1 < n) load_k(i + 1);
+                if (!two && i + 1 < n) load_k(i + 1);
                 load_v(i);
-                if (C::kScores == 1 && i + 1 < n) load_k(i + 1);
+                if (two && i + 1 < n) load_k(i + 1);
             }
             // leave no copy in flight behind
             int dummy = 0;
             for (int q = max(0, pos - C::kRing); q < pos; ++q)
                 mbar_wait(bar_full + 8 * (q % C::kRing), (q / C::kRing) & 1, &dummy, p.status, kStatusTimeoutDrain);
         }
-    } else if (warp == 4) {
+    } else if (warp == C::kSoftmax) {
         if (n > 0 && elect_one()) {
             // ------------------------------ MMA issuer ------------------------------
             constexpr uint32_t idesc_s = idesc_f16(128, 128, !CACHED, false);
             const uint32_t idesc_o = idesc_f16(128, (p.D + 15) & ~15, !CACHED, true);
             const int ksteps = (p.D + 15) >> 4;
-            bool ok = mbar_wait(bar_q, 0, abort_flag, p.status, kStatusTimeoutFull);
+            bool ok = CACHED || mbar_wait(bar_q, 0, abort_flag, p.status, kStatusTimeoutFull);
+            auto chunk = [&](int pos) { return sbase + C::kOffRing + (pos % C::kRing) * kChunk; };
             auto full = [&](int pos) {
                 ok = ok && mbar_wait(bar_full + 8 * (pos % C::kRing), (pos / C::kRing) & 1, abort_flag, p.status,
                                      kStatusTimeoutFull);
                 tc_fence_after();
-                return sbase + C::kOffRing + (pos % C::kRing) * kChunk;
             };
-            auto qk = [&](int i) {
-                const int pos = k_pos<C::kScores>(i, kc, vc), buf = i % C::kScores;
+            // With two row tiles the first waits for a chunk, the second gives it back.
+            auto qk = [&](int tile, int i) {
+                const int pos = k_pos(two, i, kc, vc), buf = two ? tile : i & 1;
                 const uint32_t d = tmem + C::kColS + buf * 128;
                 uint32_t on = 0u;
                 for (int c = 0; c < kc && ok; ++c) {
-                    const uint32_t kb = full(pos + c);
+                    if (tile == 0) full(pos + c);
                     if (!ok) break;
                     // a step of 16 elements is 32 bytes on: 2 in the descriptors' address field
-                    const uint64_t qd = desc_kmajor_sw128(sbase + c * kChunk), kd = desc_kmajor_sw128(kb);
+                    const uint64_t qd = desc_kmajor_sw128(sbase + tile * C::kQTile + c * kChunk),
+                                   kd = desc_kmajor_sw128(chunk(pos + c));
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         if (4 * c + k < ksteps) {
                             tc_mma_f16_ss(d, qd + 2 * k, kd + 2 * k, idesc_s, on);
                             on = 1u;
                         }
-                    tc_commit(bar_empty + 8 * ((pos + c) % C::kRing));
+                    if (!two || tile == 1) tc_commit(bar_empty + 8 * ((pos + c) % C::kRing));
                 }
                 tc_commit(bar_s + 8 * buf);
             };
-            qk(0);
-            for (int i = 0; i < n && ok; ++i) {
-                if (C::kScores == 2 && i + 1 < n) qk(i + 1);
-                ok = ok && mbar_wait(bar_p + 8 * (i % C::kScores), (i / C::kScores) & 1, abort_flag, p.status,
+            auto pv = [&](int tile, int i) {
+                const int buf = two ? tile : i & 1, pos = v_pos(two, i, n, kc, vc);
+                ok = ok && mbar_wait(bar_p + 8 * buf, (two ? i : i >> 1) & 1, abort_flag, p.status,
                                      kStatusTimeoutSoftmax);
-                if (!ok) break;
+                if (!ok) return;
                 tc_fence_after();
-                const int pos = v_pos<C::kScores>(i, n, kc, vc);
-                const uint32_t pt = tmem + C::kColS + (i % C::kScores) * 128;
+                const uint32_t pt = tmem + C::kColS + buf * 128;
                 uint32_t on = i > 0 ? 1u : 0u;
 #pragma unroll
                 for (int c = 0; c < vc; ++c) {
-                    const uint32_t v = full(pos + c);
+                    if (tile == 0) full(pos + c);
                     if (!ok) break;
-                    const uint64_t vd = desc_mnmajor_sw128(v, C::kKeysPerV * 128);
+                    const uint64_t vd = desc_mnmajor_sw128(chunk(pos + c), C::kKeysPerV * 128);
                     constexpr int steps = C::kKeysPerV / 16;
 #pragma unroll
                     for (int k = 0; k < steps; ++k) {  // 16 keys: 2048 bytes of V, 8 columns of P
-                        tc_mma_f16_ts(tmem, pt + 8 * (c * steps + k), vd + 128 * k, idesc_o, on);
+                        tc_mma_f16_ts(tmem + tile * 128, pt + 8 * (c * steps + k), vd + 128 * k, idesc_o, on);
                         on = 1u;
                     }
-                    tc_commit(bar_empty + 8 * ((pos + c) % C::kRing));
+                    if (!two || tile == 1) tc_commit(bar_empty + 8 * ((pos + c) % C::kRing));
                 }
-                tc_commit(i + 1 < n ? bar_o : bar_all);
-                if (C::kScores == 1 && i + 1 < n) qk(i + 1);
+                if (i + 1 < n) tc_commit(bar_o + 8 * tile);
+                else if (!two || tile == 1) tc_commit(bar_all);
+            };
+            qk(0, 0);
+            if (two) qk(1, 0);
+            for (int i = 0; i < n && ok; ++i) {
+                if (!two && i + 1 < n) qk(0, i + 1);
+                pv(0, i);
+                if (two) {
+                    if (i + 1 < n) qk(0, i + 1);
+                    pv(1, i);
+                    if (i + 1 < n) qk(1, i + 1);
+                }
             }
         }
     } else {
         // ------------------------------ Q ------------------------------
         // rows into K-major swizzled tiles (zeros past D and past the last row), all copies in flight at once
-        if (n > 0) {
-            constexpr int kUnits = DP / 8, kStep = 128 / kUnits;  // rows of a pass of the 128 threads
-            const int c = threadIdx.x % kUnits, r0 = threadIdx.x / kUnits;
+        const int tile = warp >> 3;
+        if (!CACHED && n > 0 && (tile == 0 || two)) {
+            constexpr int kUnits = DP / 8, kStep = 256 / kUnits;  // rows of a pass of the tile's 256 threads
+            const int c = threadIdx.x % kUnits, r0 = (threadIdx.x & 255) / kUnits;
+            const int first = row0 + 128 * tile;
             const uint16_t *base = p.q.ptr + b * p.q.sb + static_cast<long long>(hk) * p.G * p.q.sh + 8 * c;
             // row -> (query, head of the group), stepped without a division
             const int dt = kStep / p.G, dg = kStep - dt * p.G;
-            int t = (row0 + r0) / p.G, g = row0 + r0 - t * p.G;
-            if constexpr (CACHED) {
-                // bf16 -> fp16: a row times the power of two that brings its largest element to
-                // [2^14, 2^15) (no bit is lost that matters: what falls below fp16's range is 2^-39 of
-                // that element), the inverse goes into the row's score factor
-                constexpr int kBatch = 128 / kStep < 8 ? 128 / kStep : 8;
-                for (int rb = r0; rb < 128; rb += kBatch * kStep) {
-                    uint4 v[kBatch];
+            int t = (first + r0) / p.G, g = first + r0 - t * p.G;
 #pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        const bool in = row0 + rb + i * kStep < rows && 8 * c < p.D;
-                        v[i] = make_uint4(0u, 0u, 0u, 0u);
-                        if (in) v[i] = __ldcg(reinterpret_cast<const uint4 *>(base + t * p.q.st + g * p.q.sh));
-                        t += dt;
-                        g += dg;
-                        if (g >= p.G) {
-                            g -= p.G;
-                            ++t;
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        const int r = rb + i * kStep;
-                        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                        float top = 0.0f;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) top = fmaxf(top, fmaxf(fabsf(bf16lo(w[k])), fabsf(bf16hi(w[k]))));
-#pragma unroll
-                        for (int d = kUnits / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                        const float up = f16_row_factor(top);
-                        uint32_t h[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) h[k] = pack_f16x2(bf16lo(w[k]) * up, bf16hi(w[k]) * up);
-                        *reinterpret_cast<uint4 *>(smem + (c >> 3) * kChunk + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
-                            make_uint4(h[0], h[1], h[2], h[3]);
-                        if (c == 0) row_factor[r] = 1.0f / up;
-                    }
+            for (int r = r0; r < 128; r += kStep) {
+                const bool in = first + r < rows && 8 * c < p.D;
+                cp_async16(sbase + tile * C::kQTile + (c >> 3) * kChunk + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                           in ? base + t * p.q.st + g * p.q.sh : p.q.ptr, in ? 16u : 0u);
+                t += dt;
+                g += dg;
+                if (g >= p.G) {
+                    g -= p.G;
+                    ++t;
                 }
-            } else {
-#pragma unroll 8
-                for (int r = r0; r < 128; r += kStep) {
-                    const bool in = row0 + r < rows && 8 * c < p.D;
-                    cp_async16(sbase + (c >> 3) * kChunk + r * 128 + (((c & 7) ^ (r & 7)) << 4),
-                               in ? base + t * p.q.st + g * p.q.sh : p.q.ptr, in ? 16u : 0u);
-                    t += dt;
-                    g += dg;
-                    if (g >= p.G) {
-                        g -= p.G;
-                        ++t;
-                    }
-                }
-                cp_async_wait_all();
             }
+            cp_async_wait_all();
             fence_proxy_async_smem();
-            if (CACHED) asm volatile("bar.sync 1, 128;" ::: "memory");  // the row factors
             mbar_arrive(bar_q);
         }
 
-        // ------------------------------ softmax, a row a thread ------------------------------
-        const bool warp_on = row0 + warp * 32 < rows;  // some row of this warp exists
-        const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-        const float c = CACHED && n > 0 ? p.scale_log2 * row_factor[threadIdx.x] : p.scale_log2;
+        // ------------------------------ softmax, half a row a thread ------------------------------
+        const int quarter = warp & 3, half = (warp >> 2) & 1;  // rows 32 * quarter + lane; keys 64 * half + 0 .. 63
+        const int row = quarter * 32 + lane, first = row0 + 128 * tile;
+        const bool warp_on = first + quarter * 32 < rows;  // some row of this warp exists
+        const int tiles = tile == 0 || two ? n : 0;  // key tiles of this row tile
+        float *const places = maxima + tile * 512;
+        const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        const uint32_t o_base = lane_base + tile * 128;
+        const float c = CACHED && n > 0 ? p.scale_log2 * row_factor[row] : p.scale_log2;
+        // the two warps of the same rows
+        auto pair_sync = [&] { asm volatile("bar.sync %0, 64;" ::"r"(1 + 4 * tile + quarter) : "memory"); };
+        // the other half's value; the i-th exchange.  A place per half and parity of i: no half can be two
+        // exchanges ahead.
+        auto exchange = [&](float v, int i) {
+            float *ex = places + (i & 1) * 256 + row;
+            ex[half * 128] = v;
+            pair_sync();
+            return ex[(half ^ 1) * 128];
+        };
         float m = -INFINITY, l = 0.0f;
         bool ok = true;
-        for (int i = 0; i < n; ++i) {
-            ok = mbar_wait(bar_s + 8 * (i % C::kScores), (i / C::kScores) & 1, abort_flag, p.status,
-                           kStatusTimeoutAccum);
+        for (int i = 0; i < tiles; ++i) {
+            const int sb = two ? tile : i & 1;  // score tile
+            ok = mbar_wait(bar_s + 8 * sb, (two ? i : i >> 1) & 1, abort_flag, p.status, kStatusTimeoutAccum);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
             const int j0 = (tile0 + i) << 7;
             const bool part = p.mask != nullptr || j0 + 128 > len;
-            uint32_t keep[4];
+            uint32_t keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
             if (part) {
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    const int j = j0 + 32 * w + lane;
+                for (int w = 0; w < 2; ++w) {
+                    const int j = j0 + 64 * half + 32 * w + lane;
                     bool in = j < len;
                     if (in && p.mask != nullptr) in = __ldcg(p.mask + b * p.mask_stride + j) != 0;
                     keep[w] = __ballot_sync(0xffffffffu, in);
                 }
             }
             if (warp_on) {
-                const uint32_t ts = lane_base + C::kColS + (i % C::kScores) * 128;
-                // the scores stay in registers where a thread may have 255, else they are read twice
-                constexpr bool kKeep = C::kKeep;
-                uint32_t s[kKeep ? 4 : 2][32];
-                auto load = [&](uint32_t (&x)[32], int w) { tmem_ld_32x32b_x32(ts + 32 * w, x); };
-                auto leave_out = [&](uint32_t (&x)[32], int w) {
-                    if (part) {
-                        const uint32_t k = w == 0 ? keep[0] : w == 1 ? keep[1] : w == 2 ? keep[2] : keep[3];
+                const uint32_t buf = lane_base + C::kColS + sb * 128;
+                uint32_t s[2][32];
+                tmem_ld_32x32b_x32(buf + 64 * half, s[0]);
+                tmem_ld_32x32b_x32(buf + 64 * half + 32, s[1]);
+                tmem_ld_wait();
+                if (part) {
+#pragma unroll
+                    for (int w = 0; w < 2; ++w)
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            if (((k >> j) & 1u) == 0u) x[j] = 0xFF800000u;
-                    }
-                };
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                auto top_of = [&](const uint32_t (&x)[32]) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(x[j]));
-                };
-                if constexpr (kKeep) {
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) load(s[w], w);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        leave_out(s[w], w);
-                        top_of(s[w]);
-                    }
-                } else {
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        load(s[0], 2 * half);
-                        load(s[1], 2 * half + 1);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int w = 0; w < 2; ++w) {
-                            leave_out(s[w], 2 * half + w);
-                            top_of(s[w]);
-                        }
-                    }
+                            if (((keep[w] >> j) & 1u) == 0u) s[w][j] = 0xFF800000u;
                 }
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int w = 0; w < 2; ++w)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(s[w][j]));
+                // the row's maximum over both halves (which also orders the other half's reads of its scores
+                // before this half's weights overwrite some of them)
+                const float mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                const float top = fmaxf(mine, exchange(mine, i));
                 // the reference: the first maximum, then only one that outgrew it
                 const bool grow = top > m && !((top - m) * c <= kLazy);
                 if (__any_sync(0xffffffffu, grow)) {
                     const float f = grow ? ex2((m - top) * c) : 1.0f;
                     if (grow) m = top;
                     if (i > 0) {
-                        ok = mbar_wait(bar_o, (i - 1) & 1, abort_flag, p.status, kStatusTimeoutAccum);
+                        ok = mbar_wait(bar_o + 8 * tile, (i - 1) & 1, abort_flag, p.status, kStatusTimeoutAccum);
                         if (!__all_sync(0xffffffffu, ok)) break;
                         tc_fence_after();
                         l *= f;
-                        for (int e = 0; e < p.D; e += 32) {
-                            uint32_t o[32];
-                            tmem_ld_32x32b_x32(lane_base + e, o);
+                        for (int e = 16 * half; e < p.D; e += 32) {
+                            uint32_t o[16];
+                            tmem_ld_32x32b_x16(o_base + e, o);
                             tmem_ld_wait();
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                            tmem_st_32x32b_x32(lane_base + e, o);
+                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                            tmem_st_32x32b_x16(o_base + e, o);
                         }
                     }
                 }
                 const float mc = m == -INFINITY ? 0.0f : m * c;
                 float sum[4] = {};
+                uint32_t pk[32];
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t pk[32];
-                    if constexpr (!kKeep) {  // P of this half overwrites scores already read
-                        load(s[0], 2 * half);
-                        load(s[1], 2 * half + 1);
-                        tmem_ld_wait();
-                        leave_out(s[0], 2 * half);
-                        leave_out(s[1], 2 * half + 1);
+                for (int w = 0; w < 2; ++w)
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const float x = ex2(fmaf(__uint_as_float(s[w][j]), c, -mc));
+                        const float y = ex2(fmaf(__uint_as_float(s[w][j + 1]), c, -mc));
+                        sum[2 * w] += x;
+                        sum[2 * w + 1] += y;
+                        pk[16 * w + j / 2] = CACHED ? pack_f16x2(x, y) : pack_bf16x2_rn(x, y);
                     }
-#pragma unroll
-                    for (int w = 0; w < 2; ++w)
-#pragma unroll
-                        for (int j = 0; j < 32; j += 2) {
-                            const uint32_t *sw = s[kKeep ? 2 * half + w : w];
-                            const float x = ex2(fmaf(__uint_as_float(sw[j]), c, -mc));
-                            const float y = ex2(fmaf(__uint_as_float(sw[j + 1]), c, -mc));
-                            sum[2 * w] += x;
-                            sum[2 * w + 1] += y;
-                            pk[16 * w + j / 2] = CACHED ? pack_f16x2(x, y) : pack_bf16x2_rn(x, y);
-                        }
-                    tmem_st_32x32b_x32(ts + 32 * half, pk);
-                }
+                tmem_st_32x32b_x32(buf + 32 * half, pk);
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 tmem_st_wait();
             }
-            if (part && !CACHED) {
-                // this thread's key row of V: zeros if the key is left out.  Once the previous product is
-                // done every chunk before V's has landed, so the phase waited for is V's own.
-                if (((keep[warp] >> lane) & 1u) == 0u) {
+            if (part && !CACHED && tile == 0) {
+                // a thread's key row of V (this half's keys, 64 of them): zeros if the key is left out.  Once
+                // the previous product is done every chunk before V's has landed, so the phase waited for is V's own.
+                const int key = 64 * half + 32 * (quarter & 1) + lane;
+                if (quarter < 2 && ((keep[quarter & 1] >> lane) & 1u) == 0u) {
                     if (i > 0) ok = mbar_wait(bar_o, (i - 1) & 1, abort_flag, p.status, kStatusTimeoutAccum);
-                    const int key = threadIdx.x, pos = v_pos<C::kScores>(i, n, kc, vc) + key / C::kKeysPerV;
+                    const int pos = v_pos(two, i, n, kc, vc) + key / C::kKeysPerV;
                     ok = ok && mbar_wait(bar_full + 8 * (pos % C::kRing), (pos / C::kRing) & 1, abort_flag,
                                          p.status, kStatusTimeoutFull);
                     uint8_t *v = smem + C::kOffRing + (pos % C::kRing) * kChunk + (key % C::kKeysPerV) * 128;
@@ -545,47 +558,41 @@ __global__ void __launch_bounds__(Cfg<DP, CACHED>::kThreads, Cfg<DP, CACHED>::kC
             }
             tc_fence_before();
             // one barrier per score tile: a warp may be a tile ahead of another
-            mbar_arrive(bar_p + 8 * (i % C::kScores));
+            mbar_arrive(bar_p + 8 * sb);
         }
 
         // ------------------------------ output ------------------------------
-        // (on a barrier of its own: the one before the last may still be running, or have been done long ago)
-        if (ok && n > 0) ok = mbar_wait(bar_all, 0, abort_flag, p.status, kStatusTimeoutAccum);
+        // (of both row tiles, as the ring is used for the way out; on a barrier of its own: the product before
+        // the last may still be running, or have been done long ago)
+        if (ok && tiles > 0) ok = mbar_wait(bar_all, 0, abort_flag, p.status, kStatusTimeoutAccum);
         tc_fence_after();
         if (__all_sync(0xffffffffu, ok) && warp_on) {
-            // through shared memory (the ring is idle now), so that a warp stores whole rows: a row a thread
-            // would touch 32 lines per instruction
+            // the row's sum of weights
+            const float o = exchange(l, n);
+            l = half == 0 ? l + o : o + l;  // the same sum in both
+            // rows through shared memory (the ring is idle now), each then one bulk copy: a thread's stores of
+            // its own row would touch 32 lines an instruction
             const float f = l != 0.0f ? (CACHED ? p.cache.v.g : 1.0f) / l : 0.0f;
-            const size_t row_g = (static_cast<size_t>(b) * p.Hkv + hk) * rows + row0 + warp * 32;
-            const int live = min(32, rows - row0 - warp * 32);
+            const size_t row_g = (static_cast<size_t>(b) * p.Hkv + hk) * rows + first + row;
+            const int live = min(32, rows - first - quarter * 32);
+            const int pitch = p.D * (p.splits > 1 ? 4 : 2) + 16;
+            uint8_t *st = smem + C::kOffRing + (tile * 4 + quarter) * 32 * C::kOutPitch + lane * pitch;
             if (p.splits > 1) {
-                constexpr int kPitch = DP * 4;
-                uint8_t *st = smem + C::kOffRing + warp * 32 * kPitch;
-                if (lane < live) p.part_ml[(row_g + lane) * p.splits + split] = make_float2(m * c, l);
-                if (n > 0) {
-                    for (int e = 0; e < p.D; e += 32) {
-                        uint32_t o[32];
-                        tmem_ld_32x32b_x32(lane_base + e, o);
-                        tmem_ld_wait();
+                if (half == 0 && lane < live) p.part_ml[row_g * p.splits + split] = make_float2(m * c, l);
+                for (int e = 32 * half; e < p.D && n > 0; e += 64) {
+                    uint32_t o[32];
+                    tmem_ld_32x32b_x32(o_base + e, o);
+                    tmem_ld_wait();
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            *reinterpret_cast<uint4 *>(st + lane * kPitch + (((e >> 2) + j) ^ (lane & 7)) * 16) =
+                    for (int j = 0; j < 8; ++j)
+                        if (e + 4 * j < p.D)
+                            *reinterpret_cast<uint4 *>(st + (e + 4 * j) * 4) =
                                 make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-                    }
-                    __syncwarp();
-                    const int units = p.D >> 2, lanes = units < 32 ? 32 / units : 1;  // rows an instruction
-                    const int r0 = units < 32 ? lane / units : 0, c0 = units < 32 ? lane % units : lane;
-                    for (int r = r0; r < live && r0 < lanes; r += lanes)
-                        for (int c = c0; c < units; c += 32)
-                            *reinterpret_cast<uint4 *>(p.part_o + ((row_g + r) * p.splits + split) * p.D + 4 * c) =
-                                *reinterpret_cast<const uint4 *>(st + r * kPitch + (c ^ (r & 7)) * 16);
                 }
             } else {
-                constexpr int kPitch = DP * 2;
-                uint8_t *st = smem + C::kOffRing + warp * 32 * kPitch;
-                for (int e = 0; e < p.D; e += 32) {
+                for (int e = 32 * half; e < p.D; e += 64) {
                     uint32_t o[32];
-                    tmem_ld_32x32b_x32(lane_base + e, o);
+                    tmem_ld_32x32b_x32(o_base + e, o);
                     tmem_ld_wait();
                     if (l == 0.0f) {
 #pragma unroll
@@ -598,26 +605,23 @@ __global__ void __launch_bounds__(Cfg<DP, CACHED>::kThreads, Cfg<DP, CACHED>::kC
                         for (int q = 0; q < 4; ++q)
                             w[q] = pack_bf16x2_rn(__uint_as_float(o[8 * j + 2 * q]) * f,
                                                   __uint_as_float(o[8 * j + 2 * q + 1]) * f);
-                        *reinterpret_cast<uint4 *>(st + lane * kPitch + (((e >> 3) + j) ^ (lane & 7)) * 16) =
-                            make_uint4(w[0], w[1], w[2], w[3]);
+                        if (e + 8 * j < p.D)
+                            *reinterpret_cast<uint4 *>(st + (e + 8 * j) * 2) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
-                __syncwarp();
-                const int units = p.D >> 3, lanes = 32 / units;  // units <= 32
-                const int r0 = lane / units, c = lane % units;
-                uint16_t *to = p.out.ptr + b * p.out.sb + static_cast<long long>(hk) * p.G * p.out.sh + 8 * c;
-                const int dt = lanes / p.G, dg = lanes - dt * p.G;
-                int t = (row0 + warp * 32 + r0) / p.G, g = row0 + warp * 32 + r0 - t * p.G;
-                for (int r = r0; r < live && r0 < lanes; r += lanes) {
-                    *reinterpret_cast<uint4 *>(to + t * p.out.st + g * p.out.sh) =
-                        *reinterpret_cast<const uint4 *>(st + r * kPitch + (c ^ (r & 7)) * 16);
-                    t += dt;
-                    g += dg;
-                    if (g >= p.G) {
-                        g -= p.G;
-                        ++t;
-                    }
+            }
+            fence_proxy_async_smem();
+            pair_sync();
+            if (lane / 16 == half && lane < live) {  // 16 rows a warp
+                const uint32_t src = smem_u32(st);
+                if (p.splits > 1) {
+                    if (n > 0) bulk_store(p.part_o + (row_g * p.splits + split) * p.D, src, p.D * 4);
+                } else {
+                    const int t = (first + row) / p.G, g = first + row - t * p.G;
+                    bulk_store(p.out.ptr + b * p.out.sb + t * p.out.st + (static_cast<long long>(hk) * p.G + g) * p.out.sh,
+                               src, p.D * 2);
                 }
+                bulk_store_wait();
             }
         }
     }
@@ -631,7 +635,7 @@ __global__ void __launch_bounds__(Cfg<DP, CACHED>::kThreads, Cfg<DP, CACHED>::kC
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 4) {
+    if (warp == C::kSoftmax) {
         tc_fence_after();
         tmem_dealloc(tmem, C::kTmemCols);
     }
@@ -644,7 +648,7 @@ cudaError_t launch_dp(const CUtensorMap &mk, const CUtensorMap &mv, const AttnAr
     auto *kernel = attention_tiles_kernel<DP, CACHED>;
     cudaError_t e = set_smem_limit_once(reinterpret_cast<const void *>(kernel), C::kSmem, attr_set);
     if (e != cudaSuccess) return e;
-    const long long tiles = (static_cast<long long>(a.T) * a.G + 127) / 128;
+    const long long tiles = (static_cast<long long>(a.T) * a.G + 128 * C::kTiles - 1) / (128 * C::kTiles);
     const long long ctas = tiles * a.B * a.Hkv * a.splits;
     if (ctas > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};

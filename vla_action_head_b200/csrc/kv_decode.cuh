@@ -66,10 +66,11 @@ __device__ __forceinline__ void scale2_f16x2(uint32_t bytes, uint32_t &s0, uint3
 }
 // The power of two that brings a row whose largest magnitude is `top` to [2^14, 2^15), so that bf16
 // becomes fp16 without losing a bit that matters; 1 for rows of zeros, infinities or NaN.  Its
-// inverse is a normal number.
-__device__ __forceinline__ float f16_row_factor(float top) {
+// inverse (*inverse) is a normal number.
+__device__ __forceinline__ float f16_row_factor(float top, float *inverse) {
     const int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
     const int sh = (top > 0.0f && top < INFINITY) ? min(max(14 - ex, -113), 126) : 0;
+    *inverse = __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
     return __uint_as_float(static_cast<uint32_t>(sh + 127) << 23);
 }
 
