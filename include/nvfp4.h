@@ -483,10 +483,15 @@ nvfp4_status nvfp4_qk_norm_rope(const nvfp4_qk_args *a, nvfp4_stream_t stream);
 
 /* Reads `length` rows of each sequence from row start[b] (device, [B]; NULL: 0) on back to
  * bf16: k_out, v_out [B, length, H, D], each element val(code) * dec(sf) (exact) * scale,
- * rounded once.  Rows outside [0, cache->length) are written as zeros, and reported as above.
+ * rounded once.  Rows outside [0, cache.length) are written as zeros, and reported as above.
  * Either output's ptr may be NULL. */
-nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache *cache, const int32_t *start, int length, nvfp4_heads k_out,
-                           nvfp4_heads v_out, nvfp4_stream_t stream);
+typedef struct {
+    nvfp4_kv_cache cache;
+    const int32_t *start;
+    int64_t length;
+    nvfp4_heads k_out, v_out;
+} nvfp4_kv_read_args;
+nvfp4_status nvfp4_kv_read(const nvfp4_kv_read_args *a, nvfp4_stream_t stream);
 
 typedef struct {
     int B, T;       /* sequences, queries of each */

@@ -74,8 +74,9 @@ def test_qk_refusals(L):
 
 def test_kv_read_refusals(L):
     f = lambda c=cache(), start=None, n=10, k=heads(), v=heads(): L.nvfp4_kv_read(  # noqa: E731
-        C.byref(c) if c is not None else None, start, n, k, v, None)
-    assert f(None) == INVALID and f(n=-1) == INVALID and f(cache(length=99)) == INVALID
+        C.byref(nvfp4._KvReadArgs(c, start, n, k, v)), None)
+    assert L.nvfp4_kv_read(None, None) == INVALID
+    assert f(n=-1) == INVALID and f(n=1 << 31) == INVALID and f(cache(length=99)) == INVALID
     assert f(cache(D=264)) == SHAPE and f(cache(capacity=60)) == SHAPE
     assert f(k=heads(0x10002)) == MISALIGNED and f(v=heads(sb=8)) == INVALID and f(start=0x1001) == MISALIGNED
     assert f(n=0) == 0 and f(k=heads(None), v=heads(None)) == 0

@@ -1080,9 +1080,13 @@ nvfp4_status nvfp4_qk_norm_rope(const nvfp4_qk_args *x, nvfp4_stream_t stream) {
     return from_cuda(e);
 }
 
-nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache *cache, const int32_t *start, int length, nvfp4_heads k_out,
-                           nvfp4_heads v_out, nvfp4_stream_t stream) {
-    if (cache == nullptr || length < 0 || cache->B < 0 || cache->H <= 0 || cache->D <= 0) return NVFP4_ERR_INVALID_ARG;
+nvfp4_status nvfp4_kv_read(const nvfp4_kv_read_args *x, nvfp4_stream_t stream) {
+    if (x == nullptr || x->length < 0 || x->length > 0x7FFFFFFF) return NVFP4_ERR_INVALID_ARG;
+    const nvfp4_kv_cache *cache = &x->cache;
+    const nvfp4_heads &k_out = x->k_out, &v_out = x->v_out;
+    const int32_t *start = x->start;
+    const int length = static_cast<int>(x->length);
+    if (cache->B < 0 || cache->H <= 0 || cache->D <= 0) return NVFP4_ERR_INVALID_ARG;
     ReadArgs a = {};
     nvfp4_status st = check_cache(*cache, cache->B, cache->H, cache->D, &a.cache);
     if (st != NVFP4_OK) return st;

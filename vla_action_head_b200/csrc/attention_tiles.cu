@@ -185,13 +185,58 @@ __global__ void __launch_bounds__(Cfg<DP, CACHED>::kThreads, 1)
     const int kc = (p.D + 63) >> 6;  // 64-element blocks of a head
     constexpr int vc = C::kVC;
 
-    if (CACHED && n > 0) {
+    // Cache: the chunks' pieces in the order of the ring, in turn to the dequantizing warps
+    const uint8_t *mask = p.mask != nullptr ? p.mask + b * p.mask_stride : nullptr;
+    const size_t plane = (static_cast<size_t>(b) * p.Hkv + hk) * p.cache.C;
+    const int pieces = 4 * n * (kc + vc);
+    // piece -> is it V's, tile, chunk, block of elements, first key
+    struct Piece {
+        bool is_v;
+        int row, e0, at;  // key row in the cache, element, byte offset of the block in its chunk
+    };
+    auto piece_of = [&](int x) {
+        int pos = x >> 2, tile, c;
+        const int part = x & 3;
+        bool is_v;
+        // K0 K1 V0 K2 V1 .. V(n-1)
+        if (pos < kc) {
+            is_v = false, tile = 0, c = pos;
+        } else {
+            pos -= kc;
+            const int pair = pos / (kc + vc), in = pos - pair * (kc + vc);
+            if (pair < n - 1) is_v = in >= kc, tile = is_v ? pair : pair + 1, c = is_v ? in - kc : in;
+            else is_v = true, tile = n - 1, c = in;
+        }
+        constexpr int groups = C::kKeysPerV / 32;  // pieces of a block of a V chunk
+        const int j0 = (tile0 + tile) << 7;
+        if (!is_v) return Piece{false, j0 + 32 * part, 64 * c, 32 * part * 128};
+        const int e = part / groups, r = part % groups;
+        return Piece{true, j0 + c * C::kKeysPerV + 32 * r, 64 * e, (e * C::kKeysPerV + 32 * r) * 128};
+    };
+    auto fetch = [&](int x) {
+        if (x >= pieces) return Codes{};
+        const Piece f = piece_of(x);
+        const int j = f.row + lane;
+        bool on = j < len && f.e0 < p.D;
+        if (on && f.is_v && mask != nullptr) on = __ldcg(mask + j) != 0;
+        return load_codes(f.is_v ? p.cache.v : p.cache.k, plane + j, f.e0, p.D, on);
+    };
+    Codes codes[CACHED ? kAhead : 1];
+    const int x0 = warp - C::kSoftmax - 1;
+    if (CACHED && warp > C::kSoftmax) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) codes[CACHED ? i : 0] = fetch(x0 + i * kDequant);
+    }
+    if constexpr (CACHED) if (n > 0) {
         // Q: bf16 -> fp16 by all warps, a row times the power of two that brings its largest element to
         // [2^14, 2^15) (what falls below fp16's range is 2^-39 of that element); the inverse goes into the
         // row's score factor.  kUnits lanes a row, several rows in flight.
-        constexpr int kUnits = DP / 8, kStep = C::kThreads / kUnits, kBatch = 4;
+        constexpr int kUnits = DP / 8, kStep = C::kThreads / kUnits, kBatch = 128 / kStep < 8 ? 128 / kStep : 8;
         const int c = threadIdx.x % kUnits, r0 = threadIdx.x / kUnits;
         const uint16_t *base = p.q.ptr + b * p.q.sb + static_cast<long long>(hk) * p.G * p.q.sh + 8 * c;
+        static_assert(128 % (kBatch * kStep) == 0 && kBatch % 2 == 0, "whole batches");
+        const int dt = kStep / p.G, dg = kStep - dt * p.G;
+        int t = (row0 + r0) / p.G, g = row0 + r0 - t * p.G;
         for (int rb = r0; rb < 128; rb += kBatch * kStep) {
             uint4 v[kBatch];
             uint32_t top[kBatch];  // magnitudes as bf16 bits, which order as integers
@@ -199,9 +244,13 @@ __global__ void __launch_bounds__(Cfg<DP, CACHED>::kThreads, 1)
             for (int i = 0; i < kBatch; ++i) {
                 const int row = row0 + rb + i * kStep;
                 v[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (rb + i * kStep < 128 && row < rows && 8 * c < p.D) {
-                    const int t = row / p.G, g = row - t * p.G;
+                if (row < rows && 8 * c < p.D)
                     v[i] = __ldcg(reinterpret_cast<const uint4 *>(base + t * p.q.st + g * p.q.sh));
+                t += dt;
+                g += dg;
+                if (g >= p.G) {
+                    g -= p.G;
+                    ++t;
                 }
             }
 #pragma unroll
@@ -221,7 +270,6 @@ __global__ void __launch_bounds__(Cfg<DP, CACHED>::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
                 const int r = rb + i * kStep;
-                if (r >= 128) break;
                 float down;
                 const float up = f16_row_factor(__uint_as_float(top[i]), &down);
                 const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
@@ -239,46 +287,6 @@ __global__ void __launch_bounds__(Cfg<DP, CACHED>::kThreads, 1)
 
     if (CACHED && warp > C::kSoftmax) {
         // ------------------------------ dequantizers ------------------------------
-        // the chunks' pieces in the order of the ring, in turn to the warps
-        const uint8_t *mask = p.mask != nullptr ? p.mask + b * p.mask_stride : nullptr;
-        const size_t plane = (static_cast<size_t>(b) * p.Hkv + hk) * p.cache.C;
-        const int pieces = 4 * n * (kc + vc);
-        // piece -> is it V's, tile, chunk, block of elements, first key
-        struct Piece {
-            bool is_v;
-            int row, e0, at;  // key row in the cache, element, byte offset of the block in its chunk
-        };
-        auto piece_of = [&](int x) {
-            int pos = x >> 2, tile, c;
-            const int part = x & 3;
-            bool is_v;
-            // K0 K1 V0 K2 V1 .. V(n-1)
-            if (pos < kc) {
-                is_v = false, tile = 0, c = pos;
-            } else {
-                pos -= kc;
-                const int pair = pos / (kc + vc), in = pos - pair * (kc + vc);
-                if (pair < n - 1) is_v = in >= kc, tile = is_v ? pair : pair + 1, c = is_v ? in - kc : in;
-                else is_v = true, tile = n - 1, c = in;
-            }
-            constexpr int groups = C::kKeysPerV / 32;  // pieces of a block of a V chunk
-            const int j0 = (tile0 + tile) << 7;
-            if (!is_v) return Piece{false, j0 + 32 * part, 64 * c, 32 * part * 128};
-            const int e = part / groups, r = part % groups;
-            return Piece{true, j0 + c * C::kKeysPerV + 32 * r, 64 * e, (e * C::kKeysPerV + 32 * r) * 128};
-        };
-        auto fetch = [&](int x) {
-            if (x >= pieces) return Codes{};
-            const Piece f = piece_of(x);
-            const int j = f.row + lane;
-            bool on = j < len && f.e0 < p.D;
-            if (on && f.is_v && mask != nullptr) on = __ldcg(mask + j) != 0;
-            return load_codes(f.is_v ? p.cache.v : p.cache.k, plane + j, f.e0, p.D, on);
-        };
-        Codes q[kAhead];
-        const int x0 = warp - C::kSoftmax - 1;
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) q[i] = fetch(x0 + i * kDequant);
         bool ok = true;
         for (int x = x0; x < pieces && ok; x += kAhead * kDequant) {
 #pragma unroll
@@ -289,12 +297,12 @@ __global__ void __launch_bounds__(Cfg<DP, CACHED>::kThreads, 1)
                     if (use > 0) ok = mbar_wait(bar_empty + 8 * slot, (use - 1) & 1, abort_flag, p.status, kStatusTimeoutEmpty);
                     ok = __all_sync(0xffffffffu, ok);
                     if (ok) {
-                        store_f16(smem + C::kOffRing + slot * kChunk + piece_of(y).at, lane, q[i]);
+                        store_f16(smem + C::kOffRing + slot * kChunk + piece_of(y).at, lane, codes[CACHED ? i : 0]);
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar_full + 8 * slot);
                     }
-                    q[i] = fetch(y + kAhead * kDequant);
+                    codes[CACHED ? i : 0] = fetch(y + kAhead * kDequant);
                 }
             }
         }

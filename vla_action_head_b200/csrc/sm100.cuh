@@ -158,13 +158,14 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-// Shared -> global bulk copy (16-byte aligned, a multiple of 16 bytes) and the wait for all of this thread's.
+// Shared -> global bulk copy (16-byte aligned, a multiple of 16 bytes), and the wait until all of this
+// thread's have read their source (the writes are done when the kernel is).
 __device__ __forceinline__ void bulk_store(void *dst, uint32_t src, uint32_t bytes) {
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes)
                  : "memory");
 }
 __device__ __forceinline__ void bulk_store_wait() {
-    asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
+    asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 // Brings the line holding p into this SM's L1 (no register, no wait).
 __device__ __forceinline__ void prefetch_l1(const void *p) {

@@ -75,6 +75,11 @@ class _QkArgs(C.Structure):
                 ("start", C.c_void_p), ("count", C.c_void_p), ("cache", _KVCache), ("cached", C.c_int64)]
 
 
+class _KvReadArgs(C.Structure):
+    _fields_ = [("cache", _KVCache), ("start", C.c_void_p), ("length", C.c_int64), ("k_out", _Heads),
+                ("v_out", _Heads)]
+
+
 class _AttentionArgs(C.Structure):
     _fields_ = [("B", C.c_int), ("T", C.c_int), ("S", C.c_int), ("Hq", C.c_int), ("Hkv", C.c_int), ("D", C.c_int),
                 ("scale", C.c_float), ("q", _Heads), ("k", _Heads), ("v", _Heads), ("out", _Heads),
@@ -95,7 +100,7 @@ def _packer(struct_type):
     return p
 
 
-_PACK_QK, _PACK_ATTENTION, _PACK_CACHE = _packer(_QkArgs), _packer(_AttentionArgs), _packer(_KVCache)
+_PACK_QK, _PACK_ATTENTION, _PACK_READ = _packer(_QkArgs), _packer(_AttentionArgs), _packer(_KvReadArgs)
 _NO_HEADS, _NO_CACHE = (0, 0, 0, 0), (0, 0, 0, 0, 0.0, 0.0, 0, 0, 0, 0, 0)
 
 
@@ -137,7 +142,7 @@ def lib():
                                F, P, SZ, P]),
             # argument structures as bytes (packed) or by reference
             "nvfp4_qk_norm_rope": (I, [P, P]),
-            "nvfp4_kv_read": (I, [P, P, I, _Heads, _Heads, P]),
+            "nvfp4_kv_read": (I, [P, P]),
             "nvfp4_attention": (I, [P, P, SZ, P]),
             "nvfp4_attention_workspace_bytes": (SZ, [P]),
             "nvfp4_program_bytes": (SZ, [I]),
@@ -477,11 +482,14 @@ class KVCache:
             raise ValueError(f"k_codes must be [B, H, capacity, D/2], got {tuple(shape)}")
         B, H, cap, d2 = shape
         sf, dev = (B, H, cap, d2 // 8), kc.device
-        for n, t, w in (("k_codes", kc, shape), ("k_sf", ks, sf), ("v_codes", vc, shape), ("v_sf", vs, sf)):
-            if t.dtype is not u8 or t.shape != w or not t.is_contiguous():
-                raise ValueError(f"{n} must be a dense uint8 tensor of shape {tuple(w)}")
-            if t.device != dev:
-                raise ValueError(f"{n} is on {t.device}, k_codes on {dev}")
+        if not (kc.dtype is u8 and ks.dtype is u8 and vc.dtype is u8 and vs.dtype is u8 and ks.shape == sf and
+                vc.shape == shape and vs.shape == sf and ks.device == dev and vc.device == dev and vs.device == dev and
+                kc.is_contiguous() and ks.is_contiguous() and vc.is_contiguous() and vs.is_contiguous()):
+            for n, t, w in (("k_codes", kc, shape), ("k_sf", ks, sf), ("v_codes", vc, shape), ("v_sf", vs, sf)):
+                if t.dtype is not u8 or t.shape != w or not t.is_contiguous():
+                    raise ValueError(f"{n} must be a dense uint8 tensor of shape {tuple(w)}")
+                if t.device != dev:
+                    raise ValueError(f"{n} is on {t.device}, k_codes on {dev}")
         return (kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), self.k_scale, self.v_scale, B, H, cap,
                 2 * d2, cap if self.length is None else self.length)
 
@@ -629,8 +637,8 @@ def kv_read(cache: KVCache, start=None, length=None, k_out=None, v_out=None):
     shape = (c[6], c[10] if length is None else length, c[7], c[9])
     k_out, hk = _out_heads("k_out", k_out, shape, dev)
     v_out, hv = _out_heads("v_out", v_out, shape, dev)
-    _on(dev, lib().nvfp4_kv_read, _PACK_CACHE.pack(*c), _dense("start", start, torch.int32, (c[6],), dev), shape[1],
-        _Heads(*hk), _Heads(*hv))
+    _on(dev, lib().nvfp4_kv_read,
+        _PACK_READ.pack(*c, _dense("start", start, torch.int32, (c[6],), dev), shape[1], *hk, *hv))
     return k_out, v_out
 
 
@@ -668,9 +676,9 @@ def attention(q, k=None, v=None, cache: Optional[KVCache] = None, kv_len=None, k
         if S > 1 and step != 1:
             raise ValueError("key_mask: the places of a sequence must be adjacent")
         mask = key_mask.data_ptr()
-    a = _PACK_ATTENTION.pack(
-        B, T, S, Hq, Hkv, D, D ** -0.5 if scale is None else scale, *hq, *hk, *hv, *ho, _dense("kv_len", kv_len, torch.int32, (B,), dev), mask, mask_stride, *c,
-        cache is not None)
+    a = _PACK_ATTENTION.pack(B, T, S, Hq, Hkv, D, D ** -0.5 if scale is None else scale, *hq, *hk, *hv, *ho,
+                             _dense("kv_len", kv_len, torch.int32, (B,), dev), mask, mask_stride, *c,
+                             cache is not None)
     ws, need = None, lib().nvfp4_attention_workspace_bytes(a)
     if need:
         if workspace is None:
