@@ -509,16 +509,24 @@ bool make_cache_map(CUtensorMap *m, const uint8_t *codes, int D, long long rows)
 // Few rows share a key head: the row kernel; else the tile kernel.
 bool attention_few_rows(const AttnArgs &a) { return static_cast<long long>(a.T) * a.G <= kAttentionRows; }
 
+// Tile kernel: a CTA's partial rows are few enough bytes to be joined through a cluster's shared memory
+// (remote reads are slow: 16 rows of 256 out of eight parts took 8 us, a second kernel 3).
+bool attention_small_parts(const AttnArgs &a) {
+    return std::min(static_cast<long long>(a.T) * a.G, 256ll) * a.D * 4 <= 16384;
+}
+
 // Tile kernel: parts of the key range, the number of least modelled time (us).
 int attention_splits(const AttnArgs &a) {
     const int slots = sm_count_cached(), rows = !a.cached && a.D <= 128 ? 256 : 128;  // a CTA's
     const long long tiles = (static_cast<long long>(a.T) * a.G + rows - 1) / rows * a.B * a.Hkv;
     const int keys = (a.S + 127) / 128;
+    const bool small = attention_small_parts(a);
     int best = 1;
     double best_cost = 1e300;
     for (int s = 1; s <= keys && s <= slots && tiles * (s - 1) < 2 * slots; ++s) {
         const double waves = std::ceil(static_cast<double>(tiles * s) / slots);
-        const double cost = waves * ((keys + s - 1) / s * 1.2 + 3.0) + (s > 1 ? 3.0 + 0.05 * s : 0.0);
+        const double cost = waves * ((keys + s - 1) / s * 1.3 + 4.0) +
+                            (s == 1 ? 0.0 : s <= kAttentionCluster && small ? 1.5 : 4.0 + 0.05 * s);
         if (cost < best_cost) {
             best_cost = cost;
             best = s;
@@ -544,7 +552,7 @@ int attention_share(const AttnArgs &a) {
 // Rows of partial results in the workspace.
 size_t attention_part_rows(const AttnArgs &a) {
     if (a.share > 0) return static_cast<size_t>(a.share) * a.T * a.G;
-    return a.splits > 1 ? static_cast<size_t>(a.B) * a.T * a.Hq * a.splits : 0;
+    return a.splits > 1 && !a.cluster ? static_cast<size_t>(a.B) * a.T * a.Hq * a.splits : 0;
 }
 
 size_t attention_workspace(const AttnArgs &a) { return attention_part_rows(a) * (a.D + 2) * sizeof(float); }
@@ -595,6 +603,7 @@ nvfp4_status attention_args(const nvfp4_attention_args &x, AttnArgs *a, bool *em
     a->v_mul_h = a->v.sh != 0;
     a->v_mul_b = a->v.sb != 0;
     a->splits = attention_few_rows(*a) ? 1 : attention_splits(*a);
+    a->cluster = a->splits > 1 && a->splits <= kAttentionCluster && attention_small_parts(*a);
     a->warps = attention_rows_warps(a->cached, a->D);
     a->share = attention_few_rows(*a) ? attention_share(*a) : 0;
     return NVFP4_OK;

@@ -77,7 +77,8 @@ struct AttnArgs {
     int cached;
     Cache cache;
     int k_mul_h, k_mul_b, v_mul_h, v_mul_b;  // 0: that dimension is broadcast, its tensor-map size 1
-    int splits;      // tile kernel: parts of the key range; > 1: joined from part_o and part_ml
+    int splits;      // tile kernel: parts of the key range
+    int cluster;     // tile kernel: 1: the parts are a cluster, which joins them; 0: from part_o and part_ml
     int share;       // row kernel: > 0: CTAs dealt out by the lengths, joined; 0: a CTA a key head
     int warps;       // row kernel: of a CTA
     // unnormalized sums; references in units of log2 and sums of weights.
@@ -91,6 +92,7 @@ cudaError_t probe_attention();
 
 // Tensor-core tiles of 128 rows x 128 keys; maps over k and v [d, head, key, sequence] with boxes of
 // 64 x 1 x 128 x 1 and 64 x 1 x attention_v_box_rows x 1 elements.
+constexpr int kAttentionCluster = 8;  // parts that a cluster joins
 int attention_v_box_rows(int D);
 cudaError_t launch_attention_tiles(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a, cudaStream_t s);
 cudaError_t probe_attention_tiles();

@@ -5,8 +5,8 @@
 //
 // The rows of a tile are the (query, head) pairs that share a key head, query-major, so a group of
 // G heads reads its keys once.  One CTA takes one row tile (cache, or heads wider than 128) or two, and a
-// range of key tiles (the whole sequence, or one of `splits` parts whose O, m and l are joined by
-// attention_join_kernel).
+// range of key tiles: the whole sequence, or one of `splits` parts, whose O, m and l are joined in the
+// shared memory of a cluster (up to 8 parts) or by attention_join_kernel.
 //
 // Roles: eight warps per row tile own half a row a thread (64 keys; the halves exchange their maxima):
 // scores from tensor memory, softmax, P back to tensor memory as the A operand of P V, where it
@@ -139,6 +139,7 @@ __global__ void __launch_bounds__(Cfg<DP, CACHED>::kThreads, 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 1);
     float *row_factor = reinterpret_cast<float *>(smem + C::kOffRow);
     float *maxima = reinterpret_cast<float *>(smem + C::kOffMax);
+    float2 *part_ml = reinterpret_cast<float2 *>(smem);  // in a cluster, where Q was: reference, sum of weights
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     // the CTA's place: split fastest, then row tile, key head, sequence
@@ -159,8 +160,8 @@ __global__ void __launch_bounds__(Cfg<DP, CACHED>::kThreads, 1)
         }
         mbar_init(bar_s, 1);
         mbar_init(bar_s + 8, 1);
-        mbar_init(bar_p, 256);
-        mbar_init(bar_p + 8, 256);
+        mbar_init(bar_p, 8);
+        mbar_init(bar_p + 8, 8);
         mbar_init(bar_o, 1);
         mbar_init(bar_o + 8, 1);
         mbar_init(bar_all, 1);
@@ -227,64 +228,6 @@ __global__ void __launch_bounds__(Cfg<DP, CACHED>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) codes[CACHED ? i : 0] = fetch(x0 + i * kDequant);
     }
-    if constexpr (CACHED) if (n > 0) {
-        // Q: bf16 -> fp16 by all warps, a row times the power of two that brings its largest element to
-        // [2^14, 2^15) (what falls below fp16's range is 2^-39 of that element); the inverse goes into the
-        // row's score factor.  kUnits lanes a row, several rows in flight.
-        constexpr int kUnits = DP / 8, kStep = C::kThreads / kUnits, kBatch = 128 / kStep < 8 ? 128 / kStep : 8;
-        const int c = threadIdx.x % kUnits, r0 = threadIdx.x / kUnits;
-        const uint16_t *base = p.q.ptr + b * p.q.sb + static_cast<long long>(hk) * p.G * p.q.sh + 8 * c;
-        static_assert(128 % (kBatch * kStep) == 0 && kBatch % 2 == 0, "whole batches");
-        const int dt = kStep / p.G, dg = kStep - dt * p.G;
-        int t = (row0 + r0) / p.G, g = row0 + r0 - t * p.G;
-        for (int rb = r0; rb < 128; rb += kBatch * kStep) {
-            uint4 v[kBatch];
-            uint32_t top[kBatch];  // magnitudes as bf16 bits, which order as integers
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const int row = row0 + rb + i * kStep;
-                v[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (row < rows && 8 * c < p.D)
-                    v[i] = __ldcg(reinterpret_cast<const uint4 *>(base + t * p.q.st + g * p.q.sh));
-                t += dt;
-                g += dg;
-                if (g >= p.G) {
-                    g -= p.G;
-                    ++t;
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const uint32_t m2 = __vmaxu2(__vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu),
-                                             __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
-                top[i] = max(m2 & 0xFFFFu, m2 >> 16);
-            }
-#pragma unroll
-            for (int i = 0; i < kBatch; i += 2) {  // two rows a shuffle
-                uint32_t two = top[i] | (top[i + 1] << 16);
-#pragma unroll
-                for (int d = kUnits / 2; d > 0; d >>= 1) two = __vmaxu2(two, __shfl_xor_sync(0xffffffffu, two, d));
-                top[i] = two << 16;
-                top[i + 1] = two & 0xFFFF0000u;
-            }
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const int r = rb + i * kStep;
-                float down;
-                const float up = f16_row_factor(__uint_as_float(top[i]), &down);
-                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                uint32_t h[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) h[k] = pack_f16x2(bf16lo(w[k]) * up, bf16hi(w[k]) * up);
-                *reinterpret_cast<uint4 *>(smem + (c >> 3) * kChunk + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
-                    make_uint4(h[0], h[1], h[2], h[3]);
-                if (c == 0) row_factor[r] = down;
-            }
-        }
-        fence_proxy_async_smem();
-        __syncthreads();
-    }
-
     if (CACHED && warp > C::kSoftmax) {
         // ------------------------------ dequantizers ------------------------------
         bool ok = true;
@@ -354,7 +297,7 @@ __global__ void __launch_bounds__(Cfg<DP, CACHED>::kThreads, 1)
             constexpr uint32_t idesc_s = idesc_f16(128, 128, !CACHED, false);
             const uint32_t idesc_o = idesc_f16(128, (p.D + 15) & ~15, !CACHED, true);
             const int ksteps = (p.D + 15) >> 4;
-            bool ok = CACHED || mbar_wait(bar_q, 0, abort_flag, p.status, kStatusTimeoutFull);
+            bool ok = mbar_wait(bar_q, 0, abort_flag, p.status, kStatusTimeoutFull);
             auto chunk = [&](int pos) { return sbase + C::kOffRing + (pos % C::kRing) * kChunk; };
             auto full = [&](int pos) {
                 ok = ok && mbar_wait(bar_full + 8 * (pos % C::kRing), (pos / C::kRing) & 1, abort_flag, p.status,
@@ -420,7 +363,66 @@ __global__ void __launch_bounds__(Cfg<DP, CACHED>::kThreads, 1)
         }
     } else {
         // ------------------------------ Q ------------------------------
-        // rows into K-major swizzled tiles (zeros past D and past the last row), all copies in flight at once
+        // rows into K-major swizzled tiles (zeros past D and past the last row)
+        if constexpr (CACHED) if (n > 0) {
+            // bf16 -> fp16 (while the other warps decode the first keys), a row times the power of two that
+            // brings its largest element to [2^14, 2^15) (what falls below fp16's range is 2^-39 of that
+            // element); the inverse goes into the row's score factor.  kUnits lanes a row, several rows in flight.
+            constexpr int kUnits = DP / 8, kStep = 256 / kUnits, kBatch = 128 / kStep < 8 ? 128 / kStep : 8;
+            const int c = threadIdx.x % kUnits, r0 = threadIdx.x / kUnits;
+            const uint16_t *base = p.q.ptr + b * p.q.sb + static_cast<long long>(hk) * p.G * p.q.sh + 8 * c;
+            static_assert(128 % (kBatch * kStep) == 0 && kBatch % 2 == 0, "whole batches");
+            const int dt = kStep / p.G, dg = kStep - dt * p.G;
+            int t = (row0 + r0) / p.G, g = row0 + r0 - t * p.G;
+            for (int rb = r0; rb < 128; rb += kBatch * kStep) {
+                uint4 v[kBatch];
+                uint32_t top[kBatch];  // magnitudes as bf16 bits, which order as integers
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const int row = row0 + rb + i * kStep;
+                    v[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (row < rows && 8 * c < p.D)
+                        v[i] = __ldcg(reinterpret_cast<const uint4 *>(base + t * p.q.st + g * p.q.sh));
+                    t += dt;
+                    g += dg;
+                    if (g >= p.G) {
+                        g -= p.G;
+                        ++t;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const uint32_t m2 = __vmaxu2(__vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu),
+                                                 __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
+                    top[i] = max(m2 & 0xFFFFu, m2 >> 16);
+                }
+#pragma unroll
+                for (int i = 0; i < kBatch; i += 2) {  // two rows a shuffle
+                    uint32_t two = top[i] | (top[i + 1] << 16);
+#pragma unroll
+                    for (int d = kUnits / 2; d > 0; d >>= 1) two = __vmaxu2(two, __shfl_xor_sync(0xffffffffu, two, d));
+                    top[i] = two << 16;
+                    top[i + 1] = two & 0xFFFF0000u;
+                }
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const int r = rb + i * kStep;
+                    float down;
+                    const float up = f16_row_factor(__uint_as_float(top[i]), &down);
+                    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                    uint32_t h[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) h[k] = pack_f16x2(bf16lo(w[k]) * up, bf16hi(w[k]) * up);
+                    *reinterpret_cast<uint4 *>(smem + (c >> 3) * kChunk + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
+                        make_uint4(h[0], h[1], h[2], h[3]);
+                    if (c == 0) row_factor[r] = down;
+                }
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(bar_q);
+            mbar_wait(bar_q, 0, abort_flag, p.status, kStatusTimeoutFull);  // the row factors
+            __syncwarp();
+        }
         const int tile = warp >> 3;
         if (!CACHED && n > 0 && (tile == 0 || two)) {
             constexpr int kUnits = DP / 8, kStep = 256 / kUnits;  // rows of a pass of the tile's 256 threads
@@ -456,22 +458,26 @@ __global__ void __launch_bounds__(Cfg<DP, CACHED>::kThreads, 1)
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         const uint32_t o_base = lane_base + tile * 128;
         const float c = CACHED && n > 0 ? p.scale_log2 * row_factor[row] : p.scale_log2;
-        // the two warps of the same rows
-        auto pair_sync = [&] { asm volatile("bar.sync %0, 64;" ::"r"(1 + 4 * tile + quarter) : "memory"); };
-        // the other half's value; the i-th exchange.  A place per half and parity of i: no half can be two
-        // exchanges ahead.
+        // The two warps of the same rows meet (each as often as the other: no wait that gave up skips a meeting,
+        // so this one needs no limit of its own), and the other half's value at the i-th meeting (a place per
+        // half and parity of i: no half can be two meetings ahead).
+        auto meet = [&]() {
+            __syncwarp();
+            asm volatile("bar.sync %0, 64;" ::"r"(1 + 4 * tile + quarter) : "memory");
+        };
         auto exchange = [&](float v, int i) {
             float *ex = places + (i & 1) * 256 + row;
             ex[half * 128] = v;
-            pair_sync();
+            meet();
             return ex[(half ^ 1) * 128];
         };
         float m = -INFINITY, l = 0.0f;
-        bool ok = true;
         for (int i = 0; i < tiles; ++i) {
             const int sb = two ? tile : i & 1;  // score tile
-            ok = mbar_wait(bar_s + 8 * sb, (two ? i : i >> 1) & 1, abort_flag, p.status, kStatusTimeoutAccum);
-            if (!__all_sync(0xffffffffu, ok)) break;
+            // (a wait that gave up leaves no warp behind at a meeting: the loop goes on, and every later wait
+            // sees the abort flag)
+            mbar_wait(bar_s + 8 * sb, (two ? i : i >> 1) & 1, abort_flag, p.status, kStatusTimeoutAccum);
+            __syncwarp();
             tc_fence_after();
             const int j0 = (tile0 + i) << 7;
             const bool part = p.mask != nullptr || j0 + 128 > len;
@@ -513,8 +519,8 @@ __global__ void __launch_bounds__(Cfg<DP, CACHED>::kThreads, 1)
                     const float f = grow ? ex2((m - top) * c) : 1.0f;
                     if (grow) m = top;
                     if (i > 0) {
-                        ok = mbar_wait(bar_o + 8 * tile, (i - 1) & 1, abort_flag, p.status, kStatusTimeoutAccum);
-                        if (!__all_sync(0xffffffffu, ok)) break;
+                        mbar_wait(bar_o + 8 * tile, (i - 1) & 1, abort_flag, p.status, kStatusTimeoutAccum);
+                        __syncwarp();
                         tc_fence_after();
                         l *= f;
                         for (int e = 16 * half; e < p.D; e += 32) {
@@ -549,44 +555,46 @@ __global__ void __launch_bounds__(Cfg<DP, CACHED>::kThreads, 1)
                 // the previous product is done every chunk before V's has landed, so the phase waited for is V's own.
                 const int key = 64 * half + 32 * (quarter & 1) + lane;
                 if (quarter < 2 && ((keep[quarter & 1] >> lane) & 1u) == 0u) {
-                    if (i > 0) ok = mbar_wait(bar_o, (i - 1) & 1, abort_flag, p.status, kStatusTimeoutAccum);
+                    if (i > 0) mbar_wait(bar_o, (i - 1) & 1, abort_flag, p.status, kStatusTimeoutAccum);
                     const int pos = v_pos(two, i, n, kc, vc) + key / C::kKeysPerV;
-                    ok = ok && mbar_wait(bar_full + 8 * (pos % C::kRing), (pos / C::kRing) & 1, abort_flag,
+                    mbar_wait(bar_full + 8 * (pos % C::kRing), (pos / C::kRing) & 1, abort_flag,
                                          p.status, kStatusTimeoutFull);
                     uint8_t *v = smem + C::kOffRing + (pos % C::kRing) * kChunk + (key % C::kKeysPerV) * 128;
-                    if (ok)
-                        for (int e = 0; e < kc; ++e)
+                    for (int e = 0; e < kc; ++e)
 #pragma unroll
-                            for (int q = 0; q < 8; ++q)
-                                *reinterpret_cast<uint4 *>(v + e * C::kKeysPerV * 128 + ((q ^ (lane & 7)) << 4)) =
-                                    make_uint4(0u, 0u, 0u, 0u);
+                        for (int q = 0; q < 8; ++q)
+                            *reinterpret_cast<uint4 *>(v + e * C::kKeysPerV * 128 + ((q ^ (lane & 7)) << 4)) =
+                                make_uint4(0u, 0u, 0u, 0u);
                     fence_proxy_async_smem();
                 }
-                if (!__all_sync(0xffffffffu, ok)) break;
+                __syncwarp();
             }
             tc_fence_before();
             // one barrier per score tile: a warp may be a tile ahead of another
-            mbar_arrive(bar_p + 8 * sb);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_p + 8 * sb);
         }
 
         // ------------------------------ output ------------------------------
         // (of both row tiles, as the ring is used for the way out; on a barrier of its own: the product before
         // the last may still be running, or have been done long ago)
-        if (ok && tiles > 0) ok = mbar_wait(bar_all, 0, abort_flag, p.status, kStatusTimeoutAccum);
+        if (tiles > 0) mbar_wait(bar_all, 0, abort_flag, p.status, kStatusTimeoutAccum);
+        __syncwarp();
         tc_fence_after();
-        if (__all_sync(0xffffffffu, ok) && warp_on) {
+        if (warp_on) {
             // the row's sum of weights
             const float o = exchange(l, n);
             l = half == 0 ? l + o : o + l;  // the same sum in both
-            // rows through shared memory (the ring is idle now), each then one bulk copy: a thread's stores of
-            // its own row would touch 32 lines an instruction
+            // rows into shared memory (the ring is idle now): stored from here, a thread's own row, an
+            // instruction would touch 32 lines
             const float f = l != 0.0f ? (CACHED ? p.cache.v.g : 1.0f) / l : 0.0f;
             const size_t row_g = (static_cast<size_t>(b) * p.Hkv + hk) * rows + first + row;
             const int live = min(32, rows - first - quarter * 32);
             const int pitch = p.D * (p.splits > 1 ? 4 : 2) + 16;
             uint8_t *st = smem + C::kOffRing + (tile * 4 + quarter) * 32 * C::kOutPitch + lane * pitch;
             if (p.splits > 1) {
-                if (half == 0 && lane < live) p.part_ml[row_g * p.splits + split] = make_float2(m * c, l);
+                if (half == 0 && p.cluster) part_ml[first - row0 + row] = make_float2(m * c, l);
+                else if (half == 0 && lane < live) p.part_ml[row_g * p.splits + split] = make_float2(m * c, l);
                 for (int e = 32 * half; e < p.D && n > 0; e += 64) {
                     uint32_t o[32];
                     tmem_ld_32x32b_x32(o_base + e, o);
@@ -618,9 +626,10 @@ __global__ void __launch_bounds__(Cfg<DP, CACHED>::kThreads, 1)
                     }
                 }
             }
+            // and from there a row by one bulk copy (16 rows a warp)
             fence_proxy_async_smem();
-            pair_sync();
-            if (lane / 16 == half && lane < live) {  // 16 rows a warp
+            meet();
+            if (!p.cluster && lane / 16 == half && lane < live && *abort_flag == 0) {
                 const uint32_t src = smem_u32(st);
                 if (p.splits > 1) {
                     if (n > 0) bulk_store(p.part_o + (row_g * p.splits + split) * p.D, src, p.D * 4);
@@ -632,6 +641,55 @@ __global__ void __launch_bounds__(Cfg<DP, CACHED>::kThreads, 1)
                 bulk_store_wait();
             }
         }
+    }
+
+    __syncwarp();
+    if (p.cluster) {
+        // The parts of a row tile are the CTAs of a cluster: each joins its share of the rows out of all parts'
+        // shared memory, 8 columns a thread, all loads in flight together.  (Few bytes a part only: remote
+        // reads ran at 4-8 bytes a cycle.)
+        cluster_sync_all();
+        const int share = (128 * C::kTiles + p.splits - 1) / p.splits, units = p.D >> 3;
+        const int r0 = split * share, r1 = min(min(r0 + share, 128 * C::kTiles), rows - row0);
+        for (int x = threadIdx.x; x < (r1 - r0) * units; x += C::kThreads) {
+            const int r = r0 + x / units, e = x % units * 8;
+            const uint32_t ml = smem_u32(part_ml + r);
+            const uint32_t at = sbase + C::kOffRing + (r >> 5) * 32 * C::kOutPitch + (r & 31) * (p.D * 4 + 16) + e * 4;
+            float2 part[kAttentionCluster];
+            float4 y0[kAttentionCluster], y1[kAttentionCluster];
+            float M = -INFINITY;
+#pragma unroll
+            for (int q = 0; q < kAttentionCluster; ++q) {
+                part[q] = make_float2(-INFINITY, 0.0f);
+                if (q < p.splits) {
+                    part[q] = ld_dsmem_f2(mapa_shared(ml, q));
+                    y0[q] = ld_dsmem_f4(mapa_shared(at, q));
+                    y1[q] = ld_dsmem_f4(mapa_shared(at + 16, q));
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < kAttentionCluster; ++q)
+                if (part[q].y != 0.0f) M = fmaxf(M, part[q].x);
+            float sum = 0.0f, o[8] = {};
+#pragma unroll
+            for (int q = 0; q < kAttentionCluster; ++q)
+                if (part[q].y != 0.0f) {  // a part without keys holds nothing
+                    const float f = ex2(part[q].x - M);
+                    sum = fmaf(f, part[q].y, sum);
+                    const float y[8] = {y0[q].x, y0[q].y, y0[q].z, y0[q].w, y1[q].x, y1[q].y, y1[q].z, y1[q].w};
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) o[k] = fmaf(f, y[k], o[k]);
+                }
+            const float f = sum != 0.0f ? (CACHED ? p.cache.v.g : 1.0f) / sum : 0.0f;
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = pack_bf16x2_rn(o[2 * k] * f, o[2 * k + 1] * f);
+            const int t = (row0 + r) / p.G, g = row0 + r - t * p.G;
+            *reinterpret_cast<uint4 *>(p.out.ptr + b * p.out.sb + t * p.out.st +
+                                       (static_cast<long long>(hk) * p.G + g) * p.out.sh + e) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        cluster_sync_all();  // no CTA leaves while its memory is read
     }
 
     // teardown
@@ -664,11 +722,20 @@ cudaError_t launch_dp(const CUtensorMap &mk, const CUtensorMap &mv, const AttnAr
     cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attr[2];
+    int attrs = 0;
+    if (pdl_enabled()) {
+        attr[attrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[attrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (a.cluster) {
+        attr[attrs].id = cudaLaunchAttributeClusterDimension;
+        attr[attrs].val.clusterDim.x = static_cast<unsigned>(a.splits);
+        attr[attrs].val.clusterDim.y = 1;
+        attr[attrs++].val.clusterDim.z = 1;
+    }
     cfg.attrs = attr;
-    cfg.numAttrs = pdl_enabled() ? 1 : 0;
+    cfg.numAttrs = attrs;
     return cudaLaunchKernelEx(&cfg, kernel, mk, mv, a);
 }
 
