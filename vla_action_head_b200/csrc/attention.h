@@ -51,9 +51,10 @@ struct QkArgs {
     int cached;
     Cache cache;
     uint32_t *status;
-    FastDiv by_heads, by_t;  // set by the launcher
+    FastDiv by_tokens, by_t;  // set by the launcher
     uint32_t items;          // groups of lanes: below 2^31
     double inv_d;
+    float one;               // 1, which the compiler does not know
 };
 cudaError_t launch_qk_norm_rope(const QkArgs &a, cudaStream_t s);
 

@@ -13,9 +13,10 @@
 //                lane.  Wherever that holds: whole heads (R = D or 0) or adjacent pairs, D % 32 == 0.
 //   one_run      8 elements a lane; a pair's other half sits R / 16 lanes away: its packed bf16 words
 //                come by shuffle and its norm is redone.  Partial rotations by halves, D % 32 == 16.
-// Bound by instructions before memory: 64-bit index divisions and fp64 division and root were
-// most of one_run's 93 us for 16 x 968 tokens of 24 heads of 128 (190 MB); indexes by
-// multiplication, the root by Newton steps and both halves in a lane: XX us.
+// Bound by instructions before memory (72-78 % of the issue slots).  16 x 968 tokens of 24 heads of 128 (190 MB):
+// 93 us with 64-bit index divisions and fp64 division and root; 47 us with indexes by multiplication, the root by
+// Newton steps and both halves in a lane; 39 us with packed fp32 pairs and four heads a group, which is 74 % of
+// the rate that a copy reaches.  The cache write of 16 x 968 tokens of 8 + 1 + 1 heads of 256: 102, 56, 46 us.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -30,7 +31,7 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kHeads = 2;  // of a group, where there is work for all SMs
+constexpr int kHeads = 4;  // of a group, where there is work for all SMs
 
 __device__ __forceinline__ void unpack8(const uint4 &u, float (&x)[8]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -59,7 +60,8 @@ __device__ __forceinline__ uint32_t quantize_half16(const float (&y)[8], float g
     return cvt_e2m1x8(v);
 }
 
-// A group's heads of a token: up to U of q, of k or of v.
+// A group's heads of a token: up to U of q, of k or of v.  Tokens before heads, so that the groups of a warp
+// do alike.
 struct Item {
     int b, t, h0, n;  // n heads from h0; 0: no work
     bool is_q, is_v, turns, stores;
@@ -71,8 +73,8 @@ __device__ __forceinline__ Item item_of(const QkArgs &p, uint32_t item, bool fir
     Item x;
     const bool any = item < p.items;
     if (!any) item = 0;
-    const uint32_t token = p.by_heads.div(item);
-    int c = static_cast<int>(item - token * p.by_heads.d);
+    int c = static_cast<int>(p.by_tokens.div(item));
+    const uint32_t token = item - static_cast<uint32_t>(c) * p.by_tokens.d;
     x.b = static_cast<int>(p.by_t.div(token));
     x.t = static_cast<int>(token - static_cast<uint32_t>(x.b) * p.by_t.d);
     const int nq = (p.Hq + U - 1) / U, nk = (p.Hkv + U - 1) / U;
@@ -141,7 +143,82 @@ __device__ __forceinline__ void turn_adjacent(float (&n)[8], const float *cc, co
     }
 }
 
-template <int LPH, int U>
+// Two fp32 operations in one instruction, each rounded by itself.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 halves(uint64_t x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// a s + b with s = 1 or -1: a sum or a difference of one rounding.  s comes with the launch: a packed product and
+// a sum (or one that is seen to be a sum) are compiled into one operation, and with one rounding fewer some
+// results fall on the other side of a bf16 border.
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t s, uint64_t b) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(s), "l"(b));
+    return r;
+}
+struct Eight {
+    uint64_t x[4];
+};
+__device__ __forceinline__ Eight pairs_of(const uint4 &u) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    Eight e;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) e.x[j] = pair(bf16lo(w[j]), bf16hi(w[j]));
+    return e;
+}
+__device__ __forceinline__ double squares(const Eight &e) {
+    double s[2] = {};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 v = halves(e.x[j]);
+        s[0] = __fma_rn(static_cast<double>(v.x), static_cast<double>(v.x), s[0]);
+        s[1] = __fma_rn(static_cast<double>(v.y), static_cast<double>(v.y), s[1]);
+    }
+    return s[0] + s[1];
+}
+__device__ __forceinline__ void scale8(Eight &n, uint64_t rr, const Eight &gamma) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) n.x[j] = mul2(mul2(n.x[j], rr), gamma.x[j]);
+}
+__device__ __forceinline__ void turn_adjacent(Eight &n, const uint64_t *cc, const uint64_t *ss, float one) {  // 4 angles
+    const uint64_t sign = pair(-one, one);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = halves(n.x[i]), c2 = halves(cc[i >> 1]), s2 = halves(ss[i >> 1]);
+        const float c = i & 1 ? c2.y : c2.x, s = i & 1 ? s2.y : s2.x;
+        n.x[i] = fma2(mul2(pair(v.y, v.x), pair(s, s)), sign, mul2(n.x[i], pair(c, c)));
+    }
+}
+__device__ __forceinline__ uint4 pack8(const Eight &n) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 v = halves(n.x[j]);
+        w[j] = pack_bf16x2_rn(v.x, v.y);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void unpack8(const Eight &n, float (&y)[8]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 v = halves(n.x[j]);
+        y[2 * j] = v.x;
+        y[2 * j + 1] = v.y;
+    }
+}
+
+template <int LPH, int U, bool CACHED>
 __global__ void __launch_bounds__(kThreads, 4) qk_both_halves_kernel(const QkArgs p) {
     pdl_launch_dependents();
     pdl_wait();
@@ -149,80 +226,90 @@ __global__ void __launch_bounds__(kThreads, 4) qk_both_halves_kernel(const QkArg
     const Item x = item_of<U>(p, blockIdx.x * (kThreads / LPH) + threadIdx.x / LPH, l == 0);
     const bool lane_on = 16 * l < p.D && x.n > 0;
     const int half = p.D >> 1, ea = 8 * l, eb = half + 8 * l;
-    uint4 ua[U], ub[U];
-    {
-        const Heads in = x.is_q ? p.q : x.is_v ? p.v : p.k;
-        const uint16_t *src = in.ptr + x.b * in.sb + x.t * in.st + x.h0 * in.sh + ea;
-#pragma unroll
-        for (int u = 0; u < U; ++u, src += in.sh) {
-            ua[u] = ub[u] = make_uint4(0u, 0u, 0u, 0u);
-            if (lane_on && u < x.n) {
-                ua[u] = __ldcg(reinterpret_cast<const uint4 *>(src));
-                ub[u] = __ldcg(reinterpret_cast<const uint4 *>(src + half));
-            }
+    const Heads in = x.is_q ? p.q : x.is_v ? p.v : p.k;
+    const uint16_t *src = in.ptr + x.b * in.sb + x.t * in.st + x.h0 * in.sh + ea;
+    uint4 ua, ub;
+    auto load = [&](int u) {
+        ua = ub = make_uint4(0u, 0u, 0u, 0u);
+        if (lane_on && u < x.n) {
+            ua = __ldcg(reinterpret_cast<const uint4 *>(src));
+            ub = __ldcg(reinterpret_cast<const uint4 *>(src + half));
         }
-    }
+        src += in.sh;
+    };
+    load(0);
     // what the heads share: gamma and the angles
     const uint16_t *gamma = x.is_q ? p.q_gamma : p.k_gamma;
-    const uint4 ga = load_gamma(gamma + ea, gamma != nullptr && lane_on);
-    const uint4 gb = load_gamma(gamma + eb, gamma != nullptr && lane_on);
+    uint4 ga = load_gamma(gamma + ea, gamma != nullptr && lane_on);
+    uint4 gb = load_gamma(gamma + eb, gamma != nullptr && lane_on);
     const bool turn_a = x.turns && lane_on && (!p.inter || ea < p.R), turn_b = x.turns && lane_on && p.inter && eb < p.R;
-    float ca[8] = {}, sa[8] = {};  // halves: the 8 angles of a and b; adjacent: a's 4, then b's 4
+    uint64_t ca[4] = {}, sa[4] = {};  // halves: the 8 angles of a and b; adjacent: a's 4, then b's 4
     {
         const float *cs = p.table + static_cast<size_t>(x.pos) * p.R, *sn = cs + (p.R >> 1);
         const int i0 = p.inter ? ea >> 1 : ea, i1 = p.inter ? eb >> 1 : ea + 4;
+        auto four = [&](uint64_t *to, const float *from) {
+            const float4 f = __ldg(reinterpret_cast<const float4 *>(from));
+            to[0] = pair(f.x, f.y);
+            to[1] = pair(f.z, f.w);
+        };
         if (turn_a) {
-            *reinterpret_cast<float4 *>(ca) = __ldg(reinterpret_cast<const float4 *>(cs + i0));
-            *reinterpret_cast<float4 *>(sa) = __ldg(reinterpret_cast<const float4 *>(sn + i0));
+            four(ca, cs + i0);
+            four(sa, sn + i0);
         }
         if (p.inter ? turn_b : turn_a) {
-            *reinterpret_cast<float4 *>(ca + 4) = __ldg(reinterpret_cast<const float4 *>(cs + i1));
-            *reinterpret_cast<float4 *>(sa + 4) = __ldg(reinterpret_cast<const float4 *>(sn + i1));
+            four(ca + 2, cs + i1);
+            four(sa + 2, sn + i1);
         }
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
+    const Heads out = x.is_q ? p.q_out : p.k_out;
+    uint16_t *to = out.ptr + x.b * out.sb + x.t * out.st + x.h0 * out.sh + ea;
+#pragma unroll 1
+    for (int u = 0; u < U && __any_sync(0xffffffffu, u < x.n); ++u) {
         const bool on = lane_on && u < x.n;
-        float a[8], b[8];
-        unpack8(ua[u], a);
-        unpack8(ub[u], b);
+        // (gamma stays packed: kept in fp32 its 16 registers would spill)
+        asm volatile("" : "+r"(ga.x), "+r"(ga.y), "+r"(ga.z), "+r"(ga.w), "+r"(gb.x), "+r"(gb.y), "+r"(gb.z), "+r"(gb.w));
+        Eight a = pairs_of(ua), b = pairs_of(ub);
+        if (u + 1 < U) load(u + 1);  // on its way under this head's work
         if (p.norm) {
             double s = squares(a) + squares(b);
 #pragma unroll
             for (int o = LPH / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
             const float r = rsqrt_f64(__fma_rn(s, p.inv_d, static_cast<double>(p.eps)));
             if (!x.is_v) {
-                scale8(a, r, ga);
-                scale8(b, r, gb);
+                scale8(a, pair(r, r), pairs_of(ga));
+                scale8(b, pair(r, r), pairs_of(gb));
             }
         }
         if (p.inter) {
-            if (turn_a) turn_adjacent(a, ca, sa);
-            if (turn_b) turn_adjacent(b, ca + 4, sa + 4);
+            if (turn_a) turn_adjacent(a, ca, sa, p.one);
+            if (turn_b) turn_adjacent(b, ca + 2, sa + 2, p.one);
         } else if (turn_a) {  // R = D
+            const uint64_t plus = pair(p.one, p.one), minus = pair(-p.one, -p.one);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float y = a[i], z = b[i];
-                a[i] = __fsub_rn(__fmul_rn(y, ca[i]), __fmul_rn(z, sa[i]));
-                b[i] = __fadd_rn(__fmul_rn(z, ca[i]), __fmul_rn(y, sa[i]));
+            for (int i = 0; i < 4; ++i) {
+                const uint64_t y = a.x[i], z = b.x[i];
+                a.x[i] = fma2(mul2(z, sa[i]), minus, mul2(y, ca[i]));
+                b.x[i] = fma2(mul2(y, sa[i]), plus, mul2(z, ca[i]));
             }
         }
-        if (p.cached && __any_sync(0xffffffffu, x.stores)) {
+        if (CACHED && __any_sync(0xffffffffu, x.stores)) {
             const CachePlane c = x.is_v ? p.cache.v : p.cache.k;
             uint32_t fa, fb;
-            const uint32_t qa = quantize_half16(a, c.g, &fa), qb = quantize_half16(b, c.g, &fb);
+            float ya[8], yb[8];
+            unpack8(a, ya);
+            unpack8(b, yb);
+            const uint32_t qa = quantize_half16(ya, c.g, &fa), qb = quantize_half16(yb, c.g, &fb);
             if (x.stores && on) {
                 const size_t at = (static_cast<size_t>(x.b) * p.Hkv + x.h0 + u) * p.cache.C + x.row;
                 store_half16(c, at, p.D, ea, qa, fa);
                 store_half16(c, at, p.D, eb, qb, fb);
             }
         }
-        if (!x.stores && on) {
-            const Heads out = x.is_q ? p.q_out : p.k_out;
-            uint16_t *to = out.ptr + x.b * out.sb + x.t * out.st + (x.h0 + u) * out.sh;
-            *reinterpret_cast<uint4 *>(to + ea) = pack8(a);
-            *reinterpret_cast<uint4 *>(to + eb) = pack8(b);
+        if (!(CACHED && x.stores) && on) {
+            *reinterpret_cast<uint4 *>(to) = pack8(a);
+            *reinterpret_cast<uint4 *>(to + half) = pack8(b);
         }
+        to += out.sh;
     }
 }
 
@@ -310,17 +397,19 @@ __global__ void __launch_bounds__(kThreads) qk_one_run_kernel(const QkArgs p) {
     }
 }
 
-// U heads of a token a group (both_halves): they share the angles and gamma, and their loads are in
-// flight together; 1 where more would leave SMs without work or groups without a head.  (16 x 968
-// tokens of 24 heads of 128: 1, 2, 4 heads a group 61, 47, 52 us.)
+// U heads of a token a group (both_halves), which share the angles and gamma, the next head's loads under this
+// head's work; 1 where four would leave SMs without work (below three times the lanes that the SMs hold).  1, 2, 4
+// and 8 heads a group for 24 heads of 128 of B x 968 tokens: 4.7, 5.7, 7.9, 9.4 us (B = 1), 11.9, 10.7, 10.0, 14.6
+// (3), 27.9, 23.8, 21.6, 24.0 (8), and 47 (1), 44, 39.8, 39.3 (16).
 template <int LPH, int U, bool BOTH>
 cudaError_t launch_lph(QkArgs a, cudaStream_t s) {
     const uint32_t q = static_cast<uint32_t>((a.Hq + U - 1) / U), k = static_cast<uint32_t>((a.Hkv + U - 1) / U);
     const uint32_t heads = q + k * (a.cached ? 2 : 1);
     a.items = heads * static_cast<uint32_t>(a.B) * static_cast<uint32_t>(a.T);
-    a.by_heads = FastDiv(heads);
+    a.by_tokens = FastDiv(static_cast<uint32_t>(a.B) * static_cast<uint32_t>(a.T));
     a.by_t = FastDiv(static_cast<uint32_t>(a.T));
     a.inv_d = 1.0 / a.D;
+    a.one = 1.0f;
     // groups of a launch: below 2^32 / LPH threads
     const unsigned long long ctas = (static_cast<unsigned long long>(a.items) * LPH + kThreads - 1) / kThreads;
     if (ctas > 0x7FFFFFFFull) return cudaErrorInvalidValue;
@@ -333,8 +422,10 @@ cudaError_t launch_lph(QkArgs a, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl_enabled() ? 1 : 0;
-    if constexpr (BOTH) return cudaLaunchKernelEx(&cfg, qk_both_halves_kernel<LPH, U>, a);
-    else return cudaLaunchKernelEx(&cfg, qk_one_run_kernel<LPH>, a);
+    if constexpr (BOTH)
+        return cudaLaunchKernelEx(&cfg, a.cached ? qk_both_halves_kernel<LPH, U, true> : qk_both_halves_kernel<LPH, U, false>, a);
+    else
+        return cudaLaunchKernelEx(&cfg, qk_one_run_kernel<LPH>, a);
 }
 
 }  // namespace
@@ -343,7 +434,7 @@ cudaError_t launch_qk_norm_rope(const QkArgs &a, cudaStream_t s) {
     if (a.D % 32 == 0 && (a.inter || a.R == 0 || a.R == a.D)) {
         const int lanes = a.D / 16;  // 2 .. 16
         const double threads = static_cast<double>(a.B) * a.T * (a.Hq + (a.cached ? 2 : 1) * a.Hkv) * lanes;
-        const bool many = threads > 4.0 * 148 * 1024 && a.Hq % kHeads == 0 && a.Hkv % kHeads == 0;
+        const bool many = threads > 3.0 * 148 * 1024;
 #define NVFP4_LANES(N) \
     if (lanes <= N) return many ? launch_lph<N, kHeads, true>(a, s) : launch_lph<N, 1, true>(a, s);
         NVFP4_LANES(2) NVFP4_LANES(4) NVFP4_LANES(8) NVFP4_LANES(16)
