@@ -1,12 +1,12 @@
 // attention_rows.cu — attention for few query rows per key head (single tokens): up to 8 (query,
-// head) pairs share a key head's keys, and the keys are read once, straight into registers.
+// head) pairs share a key head's keys, which are read once.
 //
 //   S^T = K Q^T,  p = 2^(c S - c m),  l = sum p,  O^T += V^T P^T,  out = O / l,   c = scale log2(e)
 //
 // The work is the stream of keys and values, so the matrix instruction is the one that takes its
 // operands from registers (m16n8k16): 16 keys (or 16 elements of V) are its rows, the 8 query
-// rows its columns.  A contraction may take
-// its elements in any order as long as both sides do, so every thread takes runs of adjacent
+// rows its columns.  (On tcgen05 the 8 rows would be 8 of a tile's 128, and a cache's numbers would pass
+// through shared memory once more.)  A contraction may take its elements in any order as long as both sides do, so every thread takes runs of adjacent
 // elements: of a key the quarter of its lane % 4 (k of S^T), of a value row the eighth of its
 // lane / 4 (the rows of O^T), which makes 16-byte loads of plain rows.  The weights turn from S^T's
 // accumulator into the next operand by one 8 x 8 transposition in registers (movmatrix).
@@ -18,7 +18,9 @@
 // rows (a tensor copy whose 128-byte swizzle makes the reads above free of bank conflicts; plain
 // bulk copies where a cache row is no multiple of 16 bytes), and the warp waits on its own barrier.
 // No barrier of the CTA in the loop, a few instructions a step for the loads.  (8 sequences of 32701
-// cached keys, 256-wide heads: 71 us with loads into registers, 46 with cp.async by every thread, XX.)
+// cached keys, 256-wide heads: 71 us with loads into registers, 46 with cp.async by every thread, 34 so,
+// 31 with the CTAs dealt out by the lengths, the join of 3 us within.  Bound by the instructions that turn codes
+// into numbers, and by about 5 us of start and join.)
 //
 // The warps of a CTA are joined through shared memory.  A CTA takes a whole key head, or (long keys,
 // few heads) a piece of one, dealt out by the sequences' lengths (attention_share.cuh); the pieces are
