@@ -171,3 +171,27 @@ def test_norm_of_extreme_rows(many):
     z[..., 4] = 1.0
     y = nvfp4.qk_norm_rope(z.cuda(), None, eps=1e-6)[0].cpu()[0, 0, 0]
     assert torch.isnan(y[3]) and (y[4:] == 0).all() and (y[:3] == 0).all()
+
+
+@pytest.mark.parametrize("T", [1, 50])
+def test_scales_at_the_ends_of_fp32(T):
+    """Products of scales that fp32 cannot hold, with whole tiles left out before the first key: equal
+    weights, as the scores are equal to within what the weights resolve."""
+    B, S, Hq, Hkv, D = 2, 400, 8, 1, 256
+    m = torch.ones(B, S, dtype=torch.bool)
+    m[0, :260] = False
+    c = rand_cache(B, Hkv, S, D, k_scale=1e-30)
+    q = rand(B, T, Hq, D)
+    _, v = nvfp4.kv_read(c)
+    v = v.double().cpu()
+    for x, scale in ((q, 1e-30), (q * 2.0 ** -100, 1e-15), (torch.zeros_like(q), 3e38)):
+        out = nvfp4.attention(x.cuda(), cache=c, key_mask=m.cuda(), scale=scale)
+        for b in range(B):
+            at = v[b, m[b], 0]
+            want, A = at.mean(0), at.abs().mean(0)
+            # the sum of 400 equal weights and its division, the output's rounding; kv_read's own
+            bound = ref.BF16 * want.abs() + (ref.BF16 + 4 * (S + 64) * ref.F32) * A
+            assert ((out[b].double().cpu() - want).abs() <= bound).all()
+    k, w = rand(B, S, Hkv, D, seed=1).cuda(), rand(B, S, Hkv, D, seed=2).cuda()
+    out = nvfp4.attention(torch.zeros_like(q).cuda(), k, w, key_mask=m.cuda(), scale=3e38)
+    assert torch.isfinite(out).all()

@@ -6,6 +6,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <cstdio>
@@ -593,8 +594,12 @@ nvfp4_status attention_args(const nvfp4_attention_args &x, AttnArgs *a, bool *em
     a->D = x.D;
     a->G = x.Hq / x.Hkv;
     a->cached = static_cast<int>(x.cached);
-    a->scale_log2 = static_cast<float>(static_cast<double>(x.scale) * 1.4426950408889634 *
-                                       (a->cached ? static_cast<double>(a->cache.k.g) : 1.0));
+    // (a scale that fp32 cannot hold is the nearest that it can)
+    a->scale_log2 = static_cast<float>(std::min(
+        std::max(static_cast<double>(x.scale) * 1.4426950408889634 *
+                     (a->cached ? static_cast<double>(a->cache.k.g) : 1.0),
+                 static_cast<double>(FLT_MIN)),
+        static_cast<double>(FLT_MAX)));
     a->kv_len = x.kv_len;
     a->mask = x.key_mask;
     a->mask_stride = x.B > 1 ? x.mask_stride : 0;

@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(Cfg<DP, FULL, CACHED>::kThreads, 1)
         }
     }
     __syncthreads();
-    const float cr[2] = {p.scale_log2 * sm_q[2 * t], p.scale_log2 * sm_q[2 * t + 1]};  // of rows 2t, 2t + 1
+    const float cr[2] = {score_factor(p.scale_log2, sm_q[2 * t]), score_factor(p.scale_log2, sm_q[2 * t + 1])};  // of rows 2t, 2t + 1
 
     float o[kTiles][4] = {};
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};  // rows 2t, 2t + 1; m in units of log2

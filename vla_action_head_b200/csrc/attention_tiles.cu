@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(Cfg<DP, CACHED>::kThreads, 1)
         float *const places = maxima + tile * 512;
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         const uint32_t o_base = lane_base + tile * 128;
-        const float c = CACHED && n > 0 ? p.scale_log2 * row_factor[row] : p.scale_log2;
+        const float c = CACHED && n > 0 ? score_factor(p.scale_log2, row_factor[row]) : p.scale_log2;
         // The two warps of the same rows meet (each as often as the other: no wait that gave up skips a meeting,
         // so this one needs no limit of its own), and the other half's value at the i-th meeting (a place per
         // half and parity of i: no half can be two meetings ahead).

@@ -74,4 +74,10 @@ __device__ __forceinline__ float f16_row_factor(float top, float *inverse) {
     return __uint_as_float(static_cast<uint32_t>(sh + 127) << 23);
 }
 
+// A row's score factor: the scale times the inverse, held within fp32's normal numbers (0 and infinity times a
+// score that is infinite or 0 would be NaN).
+__device__ __forceinline__ float score_factor(float scale, float inverse) {
+    return fminf(fmaxf(scale * inverse, 1.17549435e-38f), 3.40282347e38f);
+}
+
 }  // namespace nvfp4
