@@ -536,20 +536,22 @@ __global__ void __launch_bounds__(Cfg<DP, CACHED>::kThreads, 1)
                     }
                 }
                 const float mc = m == -INFINITY ? 0.0f : m * c;
-                float sum[4] = {};
+                const uint64_t c2 = pair(c, c), shift = pair(-mc, -mc);
+                uint64_t sum[2] = {};
                 uint32_t pk[32];
 #pragma unroll
                 for (int w = 0; w < 2; ++w)
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
-                        const float x = ex2(fmaf(__uint_as_float(s[w][j]), c, -mc));
-                        const float y = ex2(fmaf(__uint_as_float(s[w][j + 1]), c, -mc));
-                        sum[2 * w] += x;
-                        sum[2 * w + 1] += y;
+                        const float2 e =
+                            halves(fma2(pair(__uint_as_float(s[w][j]), __uint_as_float(s[w][j + 1])), c2, shift));
+                        const float x = ex2(e.x), y = ex2(e.y);
+                        sum[w] = add2(sum[w], pair(x, y));
                         pk[16 * w + j / 2] = CACHED ? pack_f16x2(x, y) : pack_bf16x2_rn(x, y);
                     }
                 tmem_st_32x32b_x32(buf + 32 * half, pk);
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                const float2 l0 = halves(sum[0]), l1 = halves(sum[1]);
+                l += (l0.x + l0.y) + (l1.x + l1.y);
                 tmem_st_wait();
             }
             if (part && !CACHED && tile == 0) {

@@ -143,30 +143,9 @@ __device__ __forceinline__ void turn_adjacent(float (&n)[8], const float *cc, co
     }
 }
 
-// Two fp32 operations in one instruction, each rounded by itself.
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ float2 halves(uint64_t x) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-// a s + b with s = 1 or -1: a sum or a difference of one rounding.  s comes with the launch: a packed product and
+// Sums and differences of pairs are fma2(a, s, b) with s = 1 or -1, which is one rounding.  s comes with the launch: a packed product and
 // a sum (or one that is seen to be a sum) are compiled into one operation, and with one rounding fewer some
 // results fall on the other side of a bf16 border.
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t s, uint64_t b) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(s), "l"(b));
-    return r;
-}
 struct Eight {
     uint64_t x[4];
 };
