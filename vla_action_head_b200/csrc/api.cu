@@ -553,7 +553,8 @@ int attention_share(const AttnArgs &a) {
 // Rows of partial results in the workspace.
 size_t attention_part_rows(const AttnArgs &a) {
     if (a.share > 0) return static_cast<size_t>(a.share) * a.T * a.G;
-    return a.splits > 1 && !a.cluster ? static_cast<size_t>(a.B) * a.T * a.Hq * a.splits : 0;
+    if (a.splits == 1 || a.cluster) return 0;
+    return static_cast<size_t>(a.B) * a.Hkv * a.row_tiles() * a.splits * a.part_rows();
 }
 
 size_t attention_workspace(const AttnArgs &a) { return attention_part_rows(a) * (a.D + 2) * sizeof(float); }

@@ -83,10 +83,13 @@ struct AttnArgs {
     int share;       // row kernel: > 0: CTAs dealt out by the lengths, joined; 0: a CTA a key head
     int warps;       // row kernel: of a CTA
     // unnormalized sums; references in units of log2 and sums of weights.
-    // tile kernel: [rows of all heads, splits] (x D); row kernel: [CTAs, rows of a key head] (x D)
+    // tile kernel: [key heads, row tiles, splits, D / 4, part_rows(), 4] and [.., splits, part_rows()], so that
+    // rows in a warp's lanes are adjacent; row kernel: [CTAs, rows of a key head] (x D)
     float *part_o;
     float2 *part_ml;
     uint32_t *status;
+    __host__ __device__ int row_tiles() const { return (T * G + 127) >> 7; }
+    __host__ __device__ int part_rows() const { return T * G >= 128 ? 128 : (T * G + 31) & ~31; }
 };
 cudaError_t launch_attention_join(const AttnArgs &a, cudaStream_t s);
 cudaError_t probe_attention();

@@ -11,10 +11,65 @@ namespace nvfp4 {
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 128;  // also the rows of a tile
 
-// A warp a row: with M the largest reference of the parts that have a sum,
+// With M the largest reference of the parts that have a sum,
 // out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s (references in units of log2), in the order of s.
+
+// The tile kernel's parts: a thread a row and 8 columns; adjacent rows lie side by side.
+__global__ void __launch_bounds__(kThreads) attention_join_tiles_kernel(const AttnArgs p) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int rows = p.T * p.G, tiles = p.row_tiles(), pr = p.part_rows(), groups = p.D >> 3;
+    const int cg = static_cast<int>(blockIdx.x % groups), id = static_cast<int>(blockIdx.x / groups);
+    const int tile = id % tiles, bh = id / tiles, hk = bh % p.Hkv, b = bh / p.Hkv;
+    const int r = static_cast<int>(threadIdx.x), row = tile * 128 + r;
+    if (row >= rows) return;
+    const float2 *ml = p.part_ml + static_cast<size_t>(id) * p.splits * pr + r;
+    const size_t step = static_cast<size_t>(p.D >> 2) * pr;  // from a part to the next, in float4
+    const float4 *po = reinterpret_cast<const float4 *>(p.part_o) + id * p.splits * step + 2 * static_cast<size_t>(cg) * pr + r;
+    // eight parts at a time, all their loads in flight together
+    constexpr int kParts = 8;
+    float M = -INFINITY, l = 0.0f, o[8] = {};
+    for (int s0 = 0; s0 < p.splits; s0 += kParts) {
+        float2 x[kParts];
+        float4 u[kParts], v[kParts];
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+            const int s = min(s0 + i, p.splits - 1);
+            x[i] = __ldcg(ml + static_cast<size_t>(s) * pr);
+            u[i] = __ldcg(po + s * step);
+            v[i] = __ldcg(po + s * step + pr);
+            if (s0 + i >= p.splits) x[i].y = 0.0f;
+        }
+        const float before = M;
+#pragma unroll
+        for (int i = 0; i < kParts; ++i)
+            if (x[i].y != 0.0f) M = fmaxf(M, x[i].x);
+        const float g = before == -INFINITY ? 0.0f : exp2f(before - M);
+        l *= g;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[k] *= g;
+#pragma unroll
+        for (int i = 0; i < kParts; ++i)
+            if (x[i].y != 0.0f) {  // a part without keys may hold anything
+                const float f = exp2f(x[i].x - M);
+                l = fmaf(f, x[i].y, l);
+                const float y[8] = {u[i].x, u[i].y, u[i].z, u[i].w, v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                for (int k = 0; k < 8; ++k) o[k] = fmaf(f, y[k], o[k]);
+            }
+    }
+    const float f = l != 0.0f ? (p.cached ? p.cache.v.g : 1.0f) / l : 0.0f;
+    const int t = row / p.G, h = hk * p.G + row - t * p.G;
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2_rn(o[2 * i] * f, o[2 * i + 1] * f);
+    *reinterpret_cast<uint4 *>(p.out.ptr + b * p.out.sb + t * p.out.st + h * p.out.sh + 8 * cg) =
+        make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The row kernel's pieces: a warp a row.
 // The factors are found 32 parts at a time, a part a lane; the sums' loads do not wait for one another.
 __global__ void __launch_bounds__(kThreads) attention_join_kernel(const AttnArgs p) {
     pdl_launch_dependents();
@@ -26,15 +81,9 @@ __global__ void __launch_bounds__(kThreads) attention_join_kernel(const AttnArgs
     const int r = static_cast<int>(row % rows), bh = static_cast<int>(row / rows);
     const int hk = bh % p.Hkv, b = bh / p.Hkv, t = r / p.G, h = hk * p.G + r % p.G;
     // the row's parts: first index, number, and the step to the next
-    size_t first = static_cast<size_t>(row) * p.splits, step = 1;
-    int parts = p.splits;
-    if (p.share > 0) {
-        int len;
-        const int steps = key_steps(p, b, &len), piece = key_piece(p);
-        parts = (steps + piece - 1) / piece;
-        first = static_cast<size_t>(first_piece(p, b, hk, piece, steps)) * rows + r;
-        step = rows;
-    }
+    int len;
+    const int steps = key_steps(p, b, &len), piece = key_piece(p), parts = (steps + piece - 1) / piece;
+    const size_t first = static_cast<size_t>(first_piece(p, b, hk, piece, steps)) * rows + r, step = rows;
     const float2 *ml = p.part_ml + first;
     float M = -INFINITY;
     for (int s = lane; s < parts; s += 32) {
@@ -82,7 +131,8 @@ __global__ void __launch_bounds__(kThreads) attention_join_kernel(const AttnArgs
 
 cudaError_t launch_attention_join(const AttnArgs &a, cudaStream_t s) {
     const long long rows = static_cast<long long>(a.B) * a.T * a.Hq;
-    const long long ctas = (rows + kThreads / 32 - 1) / (kThreads / 32);
+    const long long ctas = a.share > 0 ? (rows + kThreads / 32 - 1) / (kThreads / 32)
+                                       : static_cast<long long>(a.B) * a.Hkv * a.row_tiles() * (a.D >> 3);
     if (ctas > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas));
@@ -93,7 +143,7 @@ cudaError_t launch_attention_join(const AttnArgs &a, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl_enabled() ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, attention_join_kernel, a);
+    return cudaLaunchKernelEx(&cfg, a.share > 0 ? attention_join_kernel : attention_join_tiles_kernel, a);
 }
 
 cudaError_t probe_attention() {

@@ -589,20 +589,36 @@ __global__ void __launch_bounds__(Cfg<DP, CACHED>::kThreads, 1)
             // the row's sum of weights
             const float o = exchange(l, n);
             l = half == 0 ? l + o : o + l;  // the same sum in both
-            // rows into shared memory (the ring is idle now): stored from here, a thread's own row, an
-            // instruction would touch 32 lines
+            // (cluster, or no parts) rows into shared memory (the ring is idle now): stored from here, a thread's
+            // own row, an instruction would touch 32 lines
             const float f = l != 0.0f ? (CACHED ? p.cache.v.g : 1.0f) / l : 0.0f;
-            const size_t row_g = (static_cast<size_t>(b) * p.Hkv + hk) * rows + first + row;
             const int live = min(32, rows - first - quarter * 32);
             const int pitch = p.D * (p.splits > 1 ? 4 : 2) + 16;
             uint8_t *st = smem + C::kOffRing + (tile * 4 + quarter) * 32 * C::kOutPitch + lane * pitch;
             if (p.splits > 1) {
+                // through the workspace: four columns of adjacent rows are adjacent, so a warp's store is 512 bytes
+                // in a row as it comes out of tensor memory
+                const int pr = p.part_rows();
+                const size_t part = ((static_cast<size_t>(b) * p.Hkv + hk) * p.row_tiles() + (first >> 7)) * p.splits + split;
+                float4 *to = reinterpret_cast<float4 *>(p.part_o) + part * (p.D >> 2) * pr + row;
                 if (half == 0 && p.cluster) part_ml[first - row0 + row] = make_float2(m * c, l);
-                else if (half == 0 && lane < live) p.part_ml[row_g * p.splits + split] = make_float2(m * c, l);
+                else if (half == 0 && lane < live) p.part_ml[part * pr + row] = make_float2(m * c, l);
                 for (int e = 32 * half; e < p.D && n > 0; e += 64) {
                     uint32_t o[32];
                     tmem_ld_32x32b_x32(o_base + e, o);
                     tmem_ld_wait();
+                    if (!p.cluster) {
+                        if (lane < live && *abort_flag == 0) {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                if (e + 4 * j < p.D)
+                                    to[static_cast<size_t>(e / 4 + j) * pr] =
+                                        make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]),
+                                                    __uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 3]));
+                        }
+                        __syncwarp();
+                        continue;
+                    }
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         if (e + 4 * j < p.D)
@@ -631,18 +647,15 @@ __global__ void __launch_bounds__(Cfg<DP, CACHED>::kThreads, 1)
                 }
             }
             // and from there a row by one bulk copy (16 rows a warp)
-            fence_proxy_async_smem();
-            meet();
-            if (!p.cluster && lane / 16 == half && lane < live && *abort_flag == 0) {
-                const uint32_t src = smem_u32(st);
-                if (p.splits > 1) {
-                    if (n > 0) bulk_store(p.part_o + (row_g * p.splits + split) * p.D, src, p.D * 4);
-                } else {
+            if (p.splits == 1) {
+                fence_proxy_async_smem();
+                meet();
+                if (lane / 16 == half && lane < live && *abort_flag == 0) {
                     const int t = (first + row) / p.G, g = first + row - t * p.G;
                     bulk_store(p.out.ptr + b * p.out.sb + t * p.out.st + (static_cast<long long>(hk) * p.G + g) * p.out.sh,
-                               src, p.D * 2);
+                               smem_u32(st), p.D * 2);
+                    bulk_store_wait();
                 }
-                bulk_store_wait();
             }
         }
     }
