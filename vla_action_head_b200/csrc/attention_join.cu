@@ -103,16 +103,22 @@ __global__ void __launch_bounds__(kThreads) attention_join_kernel(const AttnArgs
             l = fmaf(f, x.y, l);
         }
         const int n = min(32, parts - s0);
-#pragma unroll 4
-        for (int s = 0; s < n; ++s) {
-            const float fs = __shfl_sync(0xffffffffu, f, s);
-            if (e0 < p.D && fs != 0.0f) {  // a part without keys may hold anything
-                const float *q = po + (s0 + s) * step * p.D;
-                const float4 a = __ldcg(reinterpret_cast<const float4 *>(q));
-                const float4 c = __ldcg(reinterpret_cast<const float4 *>(q + 4));
-                const float y[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+        for (int s1 = 0; s1 < n; s1 += 8) {
+            float4 u[8], v[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = fmaf(fs, y[i], o[i]);
+            for (int i = 0; i < 8; ++i) {
+                const float4 *q = reinterpret_cast<const float4 *>(po + (s0 + min(s1 + i, n - 1)) * step * p.D);
+                u[i] = v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (e0 < p.D) u[i] = __ldcg(q), v[i] = __ldcg(q + 1);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float fs = s1 + i < n ? __shfl_sync(0xffffffffu, f, s1 + i) : 0.0f;
+                if (fs != 0.0f) {  // a part without keys may hold anything
+                    const float y[8] = {u[i].x, u[i].y, u[i].z, u[i].w, v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) o[k] = fmaf(fs, y[k], o[k]);
+                }
             }
         }
     }

@@ -89,6 +89,7 @@ __device__ __forceinline__ int v_pos(bool two, int i, int n, int kc, int vc) {
 // 32 bytes of codes and 4 scale bytes (zeros for keys that are left out and elements past D).
 struct Codes {
     uint32_t w[8], s;
+    int at;  // where it goes: byte offset of the 64-element block in its chunk
 };
 __device__ __forceinline__ Codes load_codes(const CachePlane &c, size_t row, int e0, int D, bool on) {
     Codes x;
@@ -222,7 +223,9 @@ __global__ void __launch_bounds__(Cfg<DP, CACHED>::kThreads, 1)
         const int j = f.row + lane;
         bool on = j < len && f.e0 < p.D;
         if (on && f.is_v && mask != nullptr) on = __ldcg(mask + j) != 0;
-        return load_codes(f.is_v ? p.cache.v : p.cache.k, plane + j, f.e0, p.D, on);
+        Codes got = load_codes(f.is_v ? p.cache.v : p.cache.k, plane + j, f.e0, p.D, on);
+        got.at = f.at;
+        return got;
     };
     Codes codes[CACHED ? kAhead : 1];
     const int x0 = warp - C::kSoftmax - 1;
@@ -242,7 +245,7 @@ __global__ void __launch_bounds__(Cfg<DP, CACHED>::kThreads, 1)
                     if (use > 0) ok = mbar_wait(bar_empty + 8 * slot, (use - 1) & 1, abort_flag, p.status, kStatusTimeoutEmpty);
                     ok = __all_sync(0xffffffffu, ok);
                     if (ok) {
-                        store_f16(smem + C::kOffRing + slot * kChunk + piece_of(y).at, lane, codes[CACHED ? i : 0]);
+                        store_f16(smem + C::kOffRing + slot * kChunk + codes[CACHED ? i : 0].at, lane, codes[CACHED ? i : 0]);
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar_full + 8 * slot);
