@@ -19,8 +19,8 @@
 // bulk copies where a cache row is no multiple of 16 bytes), and the warp waits on its own barrier.
 // No barrier of the CTA in the loop, a few instructions a step for the loads.  (8 sequences of 32701
 // cached keys, 256-wide heads: 71 us with loads into registers, 46 with cp.async by every thread, 34 so,
-// 31 with the CTAs dealt out by the lengths, the join of 3 us within.  Bound by the instructions that turn codes
-// into numbers, and by about 5 us of start and join.)
+// 31 with the CTAs dealt out by the lengths, 28.7 with the pieces joined eight at a time.  Bound by the instructions
+// that turn codes into numbers, and by about 4 us of start and join.)
 //
 // The warps of a CTA are joined through shared memory.  A CTA takes a whole key head, or (long keys,
 // few heads) a piece of one, dealt out by the sequences' lengths (attention_share.cuh); the pieces are

@@ -6,7 +6,7 @@
 // The rows of a tile are the (query, head) pairs that share a key head, query-major, so a group of
 // G heads reads its keys once.  One CTA takes one row tile (cache, or heads wider than 128) or two, and a
 // range of key tiles: the whole sequence, or one of `splits` parts, whose O, m and l are joined in the
-// shared memory of a cluster (up to 8 parts) or by attention_join_kernel.
+// shared memory of a cluster (up to 8 parts of 16 KB) or through the workspace (attention_join.cu).
 //
 // Roles: eight warps per row tile own half a row a thread (64 keys; the halves exchange their maxima):
 // scores from tensor memory, softmax, P back to tensor memory as the A operand of P V, where it
@@ -16,9 +16,9 @@
 // score tiles.  Two row tiles read each chunk of K and V once, and one's products run under the other's
 // softmax.  One row tile uses the score tiles in turn: Q K^T of the next keys runs under the softmax of these.
 // (8 x 2048 queries of 16 heads over 4096 keys of 4 heads of 128: 650 us with two CTAs per SM of one row tile
-// each and a row a thread, 551 with one CTA of two row tiles and half a row a thread.  A tile's chain of softmax
-// (2600 cycles) and products (1800) is what it waits for then: the matrix and the exponential units are both
-// busy 46 % of the time.)
+// each and a row a thread, 551 with one CTA of two row tiles and half a row a thread, 540 with scores and sums in
+// fp32 pairs.  A tile's chain of softmax (2600 cycles) and products (1800) is what it waits for then: the matrix
+// and the exponential units are both busy 46 % of the time.)
 //
 // O is rescaled only where the row maximum outgrew the reference by more than 2^8 (the weights
 // stay below 2^8, l and O are fp32; the final division cancels the reference).

@@ -13,7 +13,7 @@
 //                lane.  Wherever that holds: whole heads (R = D or 0) or adjacent pairs, D % 32 == 0.
 //   one_run      8 elements a lane; a pair's other half sits R / 16 lanes away: its packed bf16 words
 //                come by shuffle and its norm is redone.  Partial rotations by halves, D % 32 == 16.
-// Bound by instructions before memory (72-78 % of the issue slots).  16 x 968 tokens of 24 heads of 128 (190 MB):
+// Bound by instructions before memory (66-69 % of the issue slots).  16 x 968 tokens of 24 heads of 128 (190 MB):
 // 93 us with 64-bit index divisions and fp64 division and root; 47 us with indexes by multiplication, the root by
 // Newton steps and both halves in a lane; 39 us with packed fp32 pairs and four heads a group, which is 74 % of
 // the rate that a copy reaches.  The cache write of 16 x 968 tokens of 8 + 1 + 1 heads of 256: 102, 56, 46 us.
