@@ -195,3 +195,18 @@ def test_scales_at_the_ends_of_fp32(T):
     k, w = rand(B, S, Hkv, D, seed=1).cuda(), rand(B, S, Hkv, D, seed=2).cuda()
     out = nvfp4.attention(torch.zeros_like(q).cuda(), k, w, key_mask=m.cuda(), scale=3e38)
     assert torch.isfinite(out).all()
+
+
+@pytest.mark.parametrize("T", [1, 4, 70])
+@pytest.mark.parametrize("D", [8, 72, 136, 144, 168, 192, 200])
+def test_nothing_is_read_behind_a_head(T, D):
+    """Head sizes that do not fill the kernels' blocks, after a call that left NaN and infinity on every SM."""
+    B, S, H = 2, 46, 8
+    bad = [torch.full((16, n, 16, 256), x, dtype=torch.bfloat16, device="cuda") for n, x in ((T, 1.0), (600, float("nan")))]
+    q, k, v = rand(B, T, H, D), rand(B, S, H, D, seed=1), rand(B, S, H, D, seed=2)
+    want, bound = ref.attention_ref(q.double(), k.double(), v.double(), ref.default_scale(D))
+    q, k, v = q.cuda(), k.cuda(), v.cuda()
+    for x in (float("nan"), float("inf")):
+        bad[1].fill_(x)
+        nvfp4.attention(bad[0], bad[1], bad[1])
+        ref.check(nvfp4.attention(q, k, v), want, bound, (T, D, x))

@@ -360,6 +360,7 @@ __global__ void __launch_bounds__(Cfg<DP, FULL, CACHED>::kThreads, 1)
         float sa[2][4] = {};  // two chains
 #pragma unroll
         for (int i = 0; i < C::kKBlocks; ++i) {
+            if (!CACHED && (i >> 1) >= kc) break;  // blocks past the head were not brought: they hold anything
             uint32_t h0[C::kKBlock / 2], h1[C::kKBlock / 2];
             if constexpr (CACHED) {
                 codes_f16<DP, FULL, C::kKBlock>(at, at + C::kOffKs, g, C::k_element(t, i), p.D, h0);
@@ -411,6 +412,7 @@ __global__ void __launch_bounds__(Cfg<DP, FULL, CACHED>::kThreads, 1)
         // keys 2t, 2t + 1, 2t + 8, 2t + 9; zeros for the left-out ones (whatever their bytes are)
 #pragma unroll
         for (int i = 0; i < C::kVBlocks; ++i) {
+            if (!CACHED && i >= kc) break;
             // pairs of keys (2t, 2t + 1) and (2t + 8, 2t + 9): element 2x in lo[x], 2x + 1 in hi[x]
             uint32_t lo[2][C::kVBlock / 2], hi[2][C::kVBlock / 2];
 #pragma unroll
