@@ -210,3 +210,14 @@ def test_nothing_is_read_behind_a_head(T, D):
         bad[1].fill_(x)
         nvfp4.attention(bad[0], bad[1], bad[1])
         ref.check(nvfp4.attention(q, k, v), want, bound, (T, D, x))
+
+
+@pytest.mark.parametrize("T", [1, 4, 70])
+@pytest.mark.parametrize("D", [16, 48, 80, 112, 144, 208, 240])
+def test_nothing_is_read_behind_a_cached_head(orc, T, D):
+    """The same over a cache."""
+    q = torch.full((16, T, 16, 256), 1.0, dtype=torch.bfloat16, device="cuda")
+    for x in (float("nan"), float("inf")):
+        k = torch.full((16, 600, 16, 256), x, dtype=torch.bfloat16, device="cuda")
+        nvfp4.attention(q, k, k)
+        run_cache(orc, 2, T, 46, 8, 8, D)
