@@ -52,3 +52,30 @@ def test_one_key_takes_all(B, T, S, H, D, size):
         got = nvfp4.attention(q, cache=c)
         assert torch.equal(got, vc[:, at:at + 1].expand(B, T, H, D)), at
     nvfp4.device_status()
+
+
+@pytest.mark.parametrize("B", [1, 160])
+@pytest.mark.parametrize("T,Hq", [(1, 1), (1, 8), (50, 1), (20, 8)])
+def test_many_cached_keys_of_next_to_no_weight(B, T, Hq):
+    """2^18 keys of weight 2^-25.4 beside one of weight 1 and value 0: all of the result, which is 0.58 % of the
+    largest value.  (160 sequences: a CTA has the keys of a whole sequence, so the others' reference is that key.)
+
+    Bound: the weights' roundings as in attention_ref.attention_ref, but off by 2^-32 each below fp16's normal range,
+    as the largest is brought to 2^7 at least; scores are sums of 16 exact products; the sums are chains of 16 keys
+    a step at least."""
+    N, D = 1 << 18, 16
+    c = nvfp4.empty_kv_cache(B, N, 1, D)
+    c.k_codes[:, 0, 0], c.k_sf[:, 0, 0] = 0x22, 0x38  # 1.0 times a scale of 1
+    c.v_codes[:, 0, 1:], c.v_sf[:, 0, 1:] = 0x22, 0x38
+    q = torch.full((B, T, Hq, D), 1.1).bfloat16().cuda()
+    x = 16 * float(q[0, 0, 0, 0])
+    tail = (N - 1) * torch.exp(-torch.tensor(x, dtype=torch.float64))
+    want = (tail / (1 + tail)).expand(B, T, Hq, D)
+    rel = ref.BF16 + 2 * (2 * (D + 4) * ref.F32 * x) + 2 * ref.F32 * (2 * x + 8) + 4 * (N // 16 + 64) * ref.F32
+    bound = ref.BF16 * want + 1.01 * rel * want + N * 2.0 ** -32
+    ref.check(nvfp4.attention(q, cache=c, scale=1.0), want, bound)
+    # the same with the key of weight 1 somewhere else, and behind a length
+    for t in (c.k_codes, c.k_sf, c.v_codes, c.v_sf):
+        t[:, 0, [0, N - 9]] = t[:, 0, [N - 9, 0]]
+    n = torch.full((B,), N - 5, dtype=torch.int32).cuda()
+    ref.check(nvfp4.attention(q, cache=c, kv_len=n, scale=1.0), want, bound + 5.0 / N * want)

@@ -1,7 +1,7 @@
 // attention_rows.cu — attention for few query rows per key head (single tokens): up to 8 (query,
 // head) pairs share a key head's keys, which are read once.
 //
-//   S^T = K Q^T,  p = 2^(c S - c m),  l = sum p,  O^T += V^T P^T,  out = O / l,   c = scale log2(e)
+//   S^T = K Q^T,  p = 2^(c (S - m)),  l = sum p,  O^T += V^T P^T,  out = O / l,   c = scale log2(e)
 //
 // The work is the stream of keys and values, so the matrix instruction is the one that takes its
 // operands from registers (m16n8k16): 16 keys (or 16 elements of V) are its rows, the 8 query
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(Cfg<DP, FULL, CACHED>::kThreads, 1)
     const float cr[2] = {score_factor(p.scale_log2, sm_q[2 * t]), score_factor(p.scale_log2, sm_q[2 * t + 1])};  // of rows 2t, 2t + 1
 
     float o[kTiles][4] = {};
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};  // rows 2t, 2t + 1; m in units of log2
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};  // rows 2t, 2t + 1
     for (int st = step0 + warp; st < step1; st += kWarps) {
         const uint32_t keys = __ballot_sync(0xffffffffu, key != 0u);
         key = key_on(st + kWarps);
@@ -377,19 +377,20 @@ __global__ void __launch_bounds__(Cfg<DP, FULL, CACHED>::kThreads, 1)
             }
         }
         const float s[4] = {sa[0][0] + sa[1][0], sa[0][1] + sa[1][1], sa[0][2] + sa[1][2], sa[0][3] + sa[1][3]};
-        // scores in units of log2; left-out keys are -inf whatever their bytes gave
+        // scores; left-out keys are -inf whatever their bytes gave
         float x[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = ok[i >> 1] ? s[i] * cr[i & 1] : -INFINITY;
+        for (int i = 0; i < 4; ++i) x[i] = ok[i >> 1] ? s[i] : -INFINITY;
         const float top[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
-        const bool grow = (top[0] > m[0] && !(top[0] - m[0] <= kLazy)) || (top[1] > m[1] && !(top[1] - m[1] <= kLazy));
+        const bool grow = (top[0] > m[0] && !((top[0] - m[0]) * cr[0] <= kLazy)) ||
+                          (top[1] > m[1] && !((top[1] - m[1]) * cr[1] <= kLazy));
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 float n = fmaxf(m[i], top[i]);
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, d));
-                const float f = n > m[i] ? ex2(m[i] - n) : 1.0f;
+                const float f = n > m[i] ? ex2((m[i] - n) * cr[i]) : 1.0f;
                 m[i] = n;
                 l[i] *= f;
 #pragma unroll
@@ -402,7 +403,8 @@ __global__ void __launch_bounds__(Cfg<DP, FULL, CACHED>::kThreads, 1)
         float w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            w[i] = ex2(x[i] - (m[i & 1] == -INFINITY ? 0.0f : m[i & 1]));
+            const float d = x[i] - (m[i & 1] == -INFINITY ? 0.0f : m[i & 1]);
+            w[i] = ex2(CACHED ? fmaf(d, cr[i & 1], kF16WeightBits) : d * cr[i & 1]);
             l[i & 1] += w[i];
         }
         uint32_t pb[2];
@@ -454,7 +456,7 @@ __global__ void __launch_bounds__(Cfg<DP, FULL, CACHED>::kThreads, 1)
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
         if (g == 0) {
-            sm_m[warp][2 * t + i] = m[i];
+            sm_m[warp][2 * t + i] = m[i] * cr[i];  // in units of log2
             sm_l[warp][2 * t + i] = l[i];
         }
 #pragma unroll

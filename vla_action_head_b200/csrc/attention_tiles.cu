@@ -541,15 +541,15 @@ __global__ void __launch_bounds__(Cfg<DP, CACHED>::kThreads, 1)
                 // (s - m) c, not s c - m c: the rounding of a large m c would shift every weight of the row, by a
                 // factor beyond fp16 or fp32 from |m c| of 2^27 on
                 const float ref = m == -INFINITY ? 0.0f : m;
-                const uint64_t c2 = pair(c, c), shift = pair(-ref, -ref);
+                const uint64_t c2 = pair(c, c), shift = pair(-ref, -ref), up = pair(kF16WeightBits, kF16WeightBits);
                 uint64_t sum[2] = {};
                 uint32_t pk[32];
 #pragma unroll
                 for (int w = 0; w < 2; ++w)
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
-                        const float2 e = halves(
-                            mul2(add2(pair(__uint_as_float(s[w][j]), __uint_as_float(s[w][j + 1])), shift), c2));
+                        const uint64_t d = add2(pair(__uint_as_float(s[w][j]), __uint_as_float(s[w][j + 1])), shift);
+                        const float2 e = halves(CACHED ? fma2(d, c2, up) : mul2(d, c2));
                         const float x = ex2(e.x), y = ex2(e.y);
                         sum[w] = add2(sum[w], pair(x, y));
                         pk[16 * w + j / 2] = CACHED ? pack_f16x2(x, y) : pack_bf16x2_rn(x, y);

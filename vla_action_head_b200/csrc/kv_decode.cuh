@@ -80,4 +80,10 @@ __device__ __forceinline__ float score_factor(float scale, float inverse) {
     return fminf(fmaxf(scale * inverse, 1.17549435e-38f), 3.40282347e38f);
 }
 
+// Cached values take fp16 weights of up to 2^8 (what a score may outgrow its row's reference by).  Times 2^7 they
+// still fit (2^15), and a weight below 2^-32 of the reference's, not 2^-25, rounds to none: over 2^20 keys with
+// next to no weight each, what is lost is 2^-12 of the largest value at most, not 2^-5.  l and O carry the factor
+// alike, and the division takes it out.
+constexpr float kF16WeightBits = 7.0f;
+
 }  // namespace nvfp4
