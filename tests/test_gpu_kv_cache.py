@@ -251,3 +251,44 @@ def test_stream_graph_and_no_tokens():
     assert a.shape == (0, 4, 2, 64) and b.shape == (0, 4, 1, 64)
     assert nvfp4.kv_read(c, length=0)[0].shape == (1, 0, 1, 256)
     nvfp4.device_status()
+
+
+@pytest.mark.parametrize("R,D,pairs,B", [(32, 32, "half", 2), (16, 48, "half", 2), (128, 128, "inter", 3), (128, 128, "half", 400)])
+def test_a_token_that_does_not_exist_keeps_all_its_places(R, D, pairs, B):
+    """q, k, v, table and cache in one call: a token whose table row or whose cache row does not exist leaves q_out,
+    here q itself, and all four planes as they were; the other tokens are done."""
+    T, Hq, H, rows, table_rows = 8, 6, 2, 20, 30
+    table = nvfp4.rope_table(table_rows, R)
+    start = torch.tensor(([4, 16, -3] * B)[:B], dtype=torch.int32)
+    pos = torch.tensor([[0, 29, 30, 5, -1, 6, 7, 2 ** 31 - 1]] * B, dtype=torch.int32)
+    row = start[:, None] + torch.arange(T, dtype=torch.int32)
+    good = (pos >= 0) & (pos < table_rows) & (row >= 0) & (row < rows)
+    q, k, v = (rand(B, T, h, D, seed=i).cuda() for i, h in enumerate((Hq, H, H)))
+    c = nvfp4.empty_kv_cache(B, rows, H, D)
+    for t in (c.k_codes, c.k_sf, c.v_codes, c.v_sf):
+        t.fill_(0x55)
+    want_q, _ = nvfp4.qk_norm_rope(q, None, table=table, pairs=pairs, positions=pos.clamp(0, table_rows - 1).cuda())
+    want_q = torch.where(good.cuda()[:, :, None, None], want_q, q)
+    want_k, _ = nvfp4.qk_norm_rope(k, None, table=table, pairs=pairs, positions=pos.clamp(0, table_rows - 1).cuda())
+    nvfp4.device_status()
+    nvfp4.qk_norm_rope(q, k, table=table, pairs=pairs, positions=pos.cuda(), v=v, cache=c, start=start.cuda(), q_out=q)
+    with pytest.raises(nvfp4.NVFP4Error) as e:
+        nvfp4.device_status()
+    assert e.value.status == 1
+    assert torch.equal(q, want_q)
+    written = torch.zeros(B, c.k_codes.shape[2], dtype=torch.bool)
+    for b in range(min(B, 3)):
+        written[b, row[b, good[b]].long()] = True
+    for t in (c.k_codes, c.k_sf, c.v_codes, c.v_sf):
+        assert (t[:3].cpu()[~written[:3, None].expand(-1, H, -1)] == 0x55).all()
+    # the good tokens' values are there, and their keys within a code's step of the bf16 keys
+    kr, vr = nvfp4.kv_read(nvfp4.KVCache(c.k_codes, c.k_sf, c.v_codes, c.v_sf))
+    other = nvfp4.empty_kv_cache(B, T, H, D)
+    nvfp4.kv_write(other, k, v)
+    _, vo = nvfp4.kv_read(other)
+    for b in range(min(B, 3)):
+        at = good[b].nonzero()[:, 0]
+        assert torch.equal(vr[b, row[b, at].long().cuda()], vo[b, at.cuda()])
+        top = want_k[b, at.cuda()].abs().amax()
+        assert ((kr[b, row[b, at].long().cuda()] - want_k[b, at.cuda()]).abs() <= 0.3 * top).all()
+    nvfp4.device_status()

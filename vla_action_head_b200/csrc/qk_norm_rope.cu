@@ -88,8 +88,9 @@ __device__ __forceinline__ Item item_of(const QkArgs &p, uint32_t item, bool fir
     const long long pos = p.positions != nullptr ? static_cast<long long>(__ldg(p.positions + token)) : x.row;
     x.turns = p.R > 0 && !x.is_v;
     x.stores = p.cached && !x.is_q;
-    if (x.n > 0 && ((x.turns && (pos < 0 || pos >= p.table_rows)) ||
-                    (x.stores && (x.row < 0 || x.row >= p.cache.length)))) {
+    // a token's q, k and v are all left alone if its table row or its cache row does not exist
+    if (x.n > 0 && ((p.R > 0 && (pos < 0 || pos >= p.table_rows)) ||
+                    (p.cached && (x.row < 0 || x.row >= p.cache.length)))) {
         if (first_lane) atomicCAS(p.status, static_cast<uint32_t>(kStatusOk), static_cast<uint32_t>(kStatusBadIndex));
         x.n = 0;
     }
