@@ -159,3 +159,20 @@ def test_rope_table():
     t = nvfp4.rope_table(5, 8, device="cpu")
     assert t.shape == (5, 8) and torch.equal(t[0], torch.tensor([1.0] * 4 + [0.0] * 4))
     assert abs(float(t[3, 1]) - 0.955336489) < 1e-6  # cos(3 / 10)
+
+
+def test_kv_read_counts_rows_in_31_bits(L):
+    """The last CTA's rows, those behind the last one included, must not pass 2^31: their count is signed, and a
+    row that came back below 0 would be written in front of the output."""
+    def f(D, n):
+        c = cache(B=1, D=D)
+        h = heads(sb=1 << 38, st=D, sh=D)
+        return L.nvfp4_kv_read(C.byref(nvfp4._KvReadArgs(c, None, n, h, heads(None))), None)
+
+    for D in range(16, 257, 16):
+        per = 4 * (256 // (D // 8))
+        last = 2 ** 31 // per * per
+        for n in (2 ** 31 - 1, last, last + 1, last - 1):
+            if n < 2 ** 31:
+                top = (n + per - 1) // per * per - 1  # the largest row that a lane counts
+                assert f(D, n) == SHAPE if top >= 2 ** 31 else f(D, n) in NO_DEVICE, (D, n)

@@ -1113,6 +1113,9 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_read_args *x, nvfp4_stream_t stream) {
     if ((reinterpret_cast<uintptr_t>(start) & 3u) != 0) return NVFP4_ERR_MISALIGNED;
     // rows of all heads are counted in 31 bits
     if (static_cast<double>(cache->B) * length * cache->H >= 2147483648.0) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    // and so are those of the last CTA of a head, with the ones behind the last row
+    const long long per = kv_read_rows(cache->D);
+    if ((length + per - 1) / per * per > 0x80000000LL) return NVFP4_ERR_UNSUPPORTED_SHAPE;
     st = check_device();
     if (st != NVFP4_OK) return st;
     a.B = cache->B;

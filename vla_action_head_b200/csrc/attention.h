@@ -66,6 +66,7 @@ struct ReadArgs {
     uint32_t *status;
     FastDiv by_chunks, by_h;  // set by the launcher
 };
+int kv_read_rows(int D);  // rows of a CTA
 cudaError_t launch_kv_read(const ReadArgs &a, cudaStream_t s);
 
 struct AttnArgs {

@@ -72,9 +72,11 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const ReadArgs p) {
 
 }  // namespace
 
+int kv_read_rows(int D) { return kSteps * (kThreads / (D >> 3)); }
+
 cudaError_t launch_kv_read(const ReadArgs &args, cudaStream_t s) {
     ReadArgs a = args;
-    const int per = kSteps * (kThreads / (a.D >> 3));
+    const int per = kv_read_rows(a.D);
     const uint32_t chunks = static_cast<uint32_t>((a.L + static_cast<long long>(per) - 1) / per);
     a.by_chunks = FastDiv(chunks);
     a.by_h = FastDiv(a.H);
