@@ -1,6 +1,7 @@
 """Refusals of the attention-side entry points, on the CPU: the C ABI checks its arguments before
 it touches a device, the binding its tensors before it calls the library."""
 import ctypes as C
+import weakref
 
 import pytest
 import torch
@@ -176,3 +177,20 @@ def test_kv_read_counts_rows_in_31_bits(L):
             if n < 2 ** 31:
                 top = (n + per - 1) // per * per - 1  # the largest row that a lane counts
                 assert f(D, n) == SHAPE if top >= 2 ** 31 else f(D, n) in NO_DEVICE, (D, n)
+
+
+def test_a_workspace_keeps_the_buffers_it_outgrew():
+    """A graph that was captured with one holds its address; and many small steps do not pile up."""
+    ws = nvfp4.Workspace("cpu")
+    assert ws.get(0) == (None, 0)
+    first = ws.get(1000)[0]
+    at, alive = first.data_ptr(), weakref.ref(first)
+    assert ws.get(first.numel())[0] is first
+    del first
+    total = 0
+    for need in range(1 << 20, 12 << 20, 1 << 18):
+        buf, n = ws.get(need)
+        assert n >= need and not buf.any()
+        total = sum(b.numel() for b in [buf] + ws.replaced)
+    assert total < 2 * buf.numel() and buf.numel() < 2 * need
+    assert alive() is not None and alive().data_ptr() == at and not alive().any()

@@ -119,3 +119,47 @@ def test_dit_attends_to_an_encoder_and_to_itself():
         want, bound = ref.attention_ref(qkv[:, :, :32], kk, vv, 48 ** -0.5, None, m)
         ref.check(lay.context, want, bound)
         assert torch.equal(got, lay.forward(x, lay.context.view(41, 1536).clone(), y))
+
+
+@pytest.mark.parametrize("kind", [layers.ActionExpertLayer, layers.GatedActionExpertLayer])
+def test_a_captured_layer_outlives_a_longer_cache(kind):
+    """A graph per cache length, captured from one layer: a call over a longer cache in between, and what the
+    allocator then gives out, change nothing in the first graph's replay, and its replay writes only where it may."""
+    lay = kind(M=M)
+    x, y = rand(M, 1024, seed=3), torch.empty(M, 1024, dtype=torch.bfloat16, device="cuda")
+
+    def cache(rows, seed):
+        c = nvfp4.empty_kv_cache(1, rows, 1, 256)
+        nvfp4.kv_write(c, rand(1, rows, 1, 256, seed=seed), rand(1, rows, 1, 256, seed=seed + 1))
+        return layers.Attend(c, torch.tensor([rows - M], dtype=torch.int32, device="cuda"),
+                             nvfp4.rope_table(rows, 256), torch.tensor([rows], dtype=torch.int32, device="cuda"))
+
+    def run(attend):
+        if kind is layers.ActionExpertLayer:
+            return lay.forward(x, None, y, attend=attend)
+        return lay.forward(x.clone(), None, None, None, attend=attend)[0]
+
+    def need(rows):
+        a = nvfp4._AttentionArgs(B=1, T=M, S=rows, Hq=8, Hkv=1, D=256, scale=0.1, q=nvfp4._Heads(16, 0, 2048, 256),
+                                 out=nvfp4._Heads(16, 0, 2048, 256), cached=1,
+                                 cache=nvfp4._KVCache(16, 16, 16, 16, 1.0, 1.0, 1, 1, rows, 256, rows))
+        return nvfp4.lib().nvfp4_attention_workspace_bytes(nvfp4.C.byref(a))
+
+    # (the case would show nothing if the second call did not need a larger workspace)
+    assert need(8000) > 2 * need(1024) > 2 << 20
+    short, long = cache(1024, 5), cache(8000, 7)
+    want = run(short).clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = run(short)
+    run(long)
+    torch.cuda.synchronize()
+    # whatever was released is given out again
+    taken = [torch.full((n,), 7.0, dtype=torch.float32, device="cuda") for n in [1 << 18] * 40 + [1 << 20] * 8 + [need(1024) // 4]]
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        assert all(bool((t == 7).all()) for t in taken)
+    nvfp4.device_status()

@@ -313,18 +313,26 @@ def quantize_weight(w, interleave_gate_up=False, scales="amax", rotate=False, fm
 
 
 class Workspace:
-    """Caller-owned GEMM workspace: zeroed once when (re)allocated, reused across calls."""
+    """Caller-owned workspace: zeroed once when (re)allocated, reused across calls.
+
+    A buffer that became too small is kept as long as the workspace: a captured graph holds its
+    address.  Each is at least twice the last, so all of them are below twice the largest."""
 
     def __init__(self, device="cuda"):
         self.device = device
         self.buf = None
+        self.replaced = []
 
     def get(self, nbytes):
         torch = _torch()
         if nbytes == 0:
             return None, 0
         if self.buf is None or self.buf.numel() < nbytes:
-            self.buf = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=self.device)
+            least = 1 << 20
+            if self.buf is not None:
+                self.replaced.append(self.buf)
+                least = 2 * self.buf.numel()
+            self.buf = torch.zeros(max(nbytes, least), dtype=torch.uint8, device=self.device)
         return self.buf, self.buf.numel()
 
 
