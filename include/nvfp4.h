@@ -149,7 +149,8 @@ nvfp4_status nvfp4_sf_zero(uint8_t *sf, int rows, int K, nvfp4_stream_t stream);
  * partials (splits x M x N x 4 bytes; the many-row schedule rounds M up to whole 128-row
  * tiles).  A workspace must be zeroed once at allocation; every call leaves its counters
  * zero again, and no call's partials overlap the counter region, so one workspace may serve
- * GEMMs of different shapes one after another (after NVFP4_ERR_TIMEOUT, zero it again).
+ * GEMMs of different shapes, and nvfp4_attention, one after another (after NVFP4_ERR_TIMEOUT,
+ * zero it again).
  * Schedules whose counters exceed the region (more than 4096 tiles, 2048 for the many-row
  * kernel) return NVFP4_ERR_UNSUPPORTED_SHAPE. */
 size_t nvfp4_gemm_workspace_bytes(int M, int N, int K);
@@ -513,7 +514,8 @@ typedef struct {
  * statistics and sums are fp32; the softmax weights are rounded to bf16 (bf16 keys and
  * values) or fp16 (cache) for their product with the values; out is rounded once to bf16.
  * B, T, S = 0: nothing is read (S = 0: zeros are written).  Results do not depend on timing.
- * workspace: nvfp4_attention_workspace_bytes, used by one call at a time, any contents. */
+ * workspace: nvfp4_attention_workspace_bytes, used by one call at a time, any contents.  Its first
+ * 16 KiB are left alone, so a workspace of nvfp4_gemm may serve both, one after another. */
 nvfp4_status nvfp4_attention(const nvfp4_attention_args *a, void *workspace, size_t ws_bytes,
                              nvfp4_stream_t stream);
 size_t nvfp4_attention_workspace_bytes(const nvfp4_attention_args *a);

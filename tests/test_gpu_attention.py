@@ -307,3 +307,31 @@ def test_offsets_beyond_32_bits(orc):
     kr, vr = nvfp4.kv_read(c, start=start, length=n)
     assert torch.equal(kr[1].double().cpu(), k[0]) and torch.equal(vr[1].double().cpu(), v[0])
     assert np.all(kr[0].float().cpu().numpy() == 0)
+
+
+@pytest.mark.parametrize("T,S,Hq", [(1, 9000, 8), (50, 1018, 8), (50, 6000, 8)])
+def test_one_workspace_for_gemms_and_attention(T, S, Hq):
+    """GEMMs that reduce through the workspace and attention in parts, in turn on one workspace, eager and in a graph:
+    bit for bit what each gives on one of its own."""
+    q, k, v = rand(1, T, Hq, 256).cuda(), rand(1, S, 1, 256, seed=1).cuda(), rand(1, S, 1, 256, seed=2).cuda()
+    gemms = []
+    for M, N, K, splits in ((41, 1536, 6144, -1), (50, 1024, 4096, -1), (968, 2048, 16384, 0)):
+        a = nvfp4.quantize_norm(rand(M, K, seed=3).cuda(), "none")
+        w = nvfp4.quantize_weight(rand(N, K, seed=4, std=0.02).cuda())
+        assert nvfp4.lib().nvfp4_gemm_workspace_bytes_ex(M, N, K, 0, splits) > 16384
+        gemms.append(lambda ws, a=a, w=w, splits=splits: nvfp4.gemm(a, w, workspace=ws, splits=splits))
+    calls = [f for g in gemms for f in (g, lambda ws: nvfp4.attention(q, k, v, workspace=ws))]
+    want = [f(nvfp4.Workspace()) for f in calls]
+    ws = nvfp4.Workspace()
+    for _ in range(3):
+        got = [f(ws) for f in calls]
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+    assert not ws.buf[:16384].any()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = [f(ws) for f in calls]
+    for _ in range(3):
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+    nvfp4.device_status()

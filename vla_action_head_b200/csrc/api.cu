@@ -557,7 +557,11 @@ size_t attention_part_rows(const AttnArgs &a) {
     return static_cast<size_t>(a.B) * a.Hkv * a.row_tiles() * a.splits * a.part_rows();
 }
 
-size_t attention_workspace(const AttnArgs &a) { return attention_part_rows(a) * (a.D + 2) * sizeof(float); }
+// Behind the GEMMs' counters, which a workspace that serves both must keep zero.
+size_t attention_workspace(const AttnArgs &a) {
+    const size_t rows = attention_part_rows(a);
+    return rows == 0 ? 0 : kTicketRegion + rows * (a.D + 2) * sizeof(float);
+}
 
 // The arguments of nvfp4_attention, without device access; `empty`: there is nothing to write.
 nvfp4_status attention_args(const nvfp4_attention_args &x, AttnArgs *a, bool *empty) {
@@ -1146,7 +1150,7 @@ nvfp4_status nvfp4_attention(const nvfp4_attention_args *x, void *workspace, siz
     if (need > 0) {
         if (workspace == nullptr || ws_bytes < need) return NVFP4_ERR_WORKSPACE;
         if (!aligned16(workspace)) return NVFP4_ERR_MISALIGNED;
-        a.part_o = static_cast<float *>(workspace);
+        a.part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kTicketRegion);
         a.part_ml = reinterpret_cast<float2 *>(a.part_o + attention_part_rows(a) * a.D);
     }
     st = check_device();

@@ -313,7 +313,8 @@ def quantize_weight(w, interleave_gate_up=False, scales="amax", rotate=False, fm
 
 
 class Workspace:
-    """Caller-owned workspace: zeroed once when (re)allocated, reused across calls.
+    """Caller-owned workspace of GEMMs and attention calls on one stream: zeroed once when
+    (re)allocated, reused across calls.
 
     A buffer that became too small is kept as long as the workspace: a captured graph holds its
     address.  Each is at least twice the last, so all of them are below twice the largest."""
@@ -657,7 +658,8 @@ def attention(q, k=None, v=None, cache: Optional[KVCache] = None, kv_len=None, k
 
     kv_len int32 [B]: keys of each sequence (None: all rows); key_mask bool or uint8 [B, S]: False
     leaves a key out.  A query without keys gives 0.  scale defaults to 1/sqrt(D).
-    workspace: scratch, grown on demand; None takes it from the allocator for this call."""
+    workspace: scratch, grown on demand, which may be that of GEMMs on the same stream; None takes it
+    from the allocator for this call."""
     torch = _torch()
     shape = B, T, Hq, D = _four("q", q)
     dev = q.device
