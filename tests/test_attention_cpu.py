@@ -202,3 +202,9 @@ def test_parts_lie_behind_the_counters_of_gemms(L, kw):
     D = kw.get("D", 256)
     need = L.nvfp4_attention_workspace_bytes(C.byref(at(**kw)))
     assert need > 16384 and (need - 16384) % (4 * (D + 2)) == 0
+
+
+def test_a_workspace_of_another_device_is_refused(L):
+    q, k = torch.zeros(1, 1, 8, 64, dtype=torch.bfloat16), torch.zeros(1, 40000, 1, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="workspace is on meta"):
+        nvfp4.attention(q, k, k, workspace=nvfp4.Workspace("meta"))

@@ -695,5 +695,7 @@ def attention(q, k=None, v=None, cache: Optional[KVCache] = None, kv_len=None, k
             ws = torch.empty(need, dtype=torch.uint8, device=dev)
         else:
             ws, need = workspace.get(need)
+            if ws.device != dev:
+                raise ValueError(f"workspace is on {ws.device}, not on {dev}")
     _on(dev, lib().nvfp4_attention, a, None if ws is None else ws.data_ptr(), need)
     return out
