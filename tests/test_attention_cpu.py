@@ -6,7 +6,7 @@ import weakref
 import pytest
 import torch
 
-from vla_action_head_b200 import build, nvfp4
+from vla_action_head_b200 import build, layers, nvfp4
 
 INVALID, SHAPE, MISALIGNED, WORKSPACE = 1, 2, 3, 4
 NO_DEVICE = (5, 6)
@@ -208,3 +208,17 @@ def test_a_workspace_of_another_device_is_refused(L):
     q, k = torch.zeros(1, 1, 8, 64, dtype=torch.bfloat16), torch.zeros(1, 40000, 1, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="workspace is on meta"):
         nvfp4.attention(q, k, k, workspace=nvfp4.Workspace("meta"))
+
+
+def test_the_keys_of_a_layer_end_with_its_own_tokens(monkeypatch):
+    """Without a kv_len: not with the cache's last row, which may never have been written."""
+    seen = []
+    monkeypatch.setattr(nvfp4, "qk_norm_rope", lambda *a, **kw: None)
+    monkeypatch.setattr(nvfp4, "attention", lambda q, **kw: seen.append(kw["kv_len"]))
+    start = torch.tensor([7], dtype=torch.int32)
+    c = nvfp4.empty_kv_cache(1, 60, 1, 256, device="cpu")
+    step = layers._CacheAttention(4, 8, 1, 256, "cpu")
+    step(torch.zeros(4, 2560, dtype=torch.bfloat16), layers.Attend(c, start, None))
+    given = torch.tensor([9], dtype=torch.int32)
+    step(torch.zeros(4, 2560, dtype=torch.bfloat16), layers.Attend(c, start, None, given))
+    assert seen[0].tolist() == [11] and seen[0].dtype is torch.int32 and seen[1] is given

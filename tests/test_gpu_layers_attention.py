@@ -163,3 +163,24 @@ def test_a_captured_layer_outlives_a_longer_cache(kind):
         assert torch.equal(out, want)
         assert all(bool((t == 7).all()) for t in taken)
     nvfp4.device_status()
+
+
+def test_rows_behind_the_chunk_are_not_attended_to(prompt):
+    """An Attend without kv_len, over a cache that is longer than prompt and chunk and holds an older prompt's rows."""
+    _, filled = prompt
+    c = nvfp4.empty_kv_cache(1, P + M + 500, 1, 256)
+    old = rand(1, P + M + 500, 1, 256, seed=9)
+    nvfp4.kv_write(c, old, old)
+    for new, t in zip((c.k_codes, c.k_sf, c.v_codes, c.v_sf),
+                      (filled.cache.k_codes, filled.cache.k_sf, filled.cache.v_codes, filled.cache.v_sf)):
+        new[:, :, :P] = t[:, :, :P]
+    start = torch.tensor([P], dtype=torch.int32, device="cuda")
+    table = nvfp4.rope_table(P + M, 256)
+    lay = layers.ActionExpertLayer(M=M)
+    x, y = rand(M, 1024, seed=3), torch.empty(M, 1024, dtype=torch.bfloat16, device="cuda")
+    want = lay.forward(x, None, y, attend=layers.Attend(c, start, table, start + M)).clone()
+    got = lay.forward(x, None, y, attend=layers.Attend(c, start, table)).clone()
+    assert torch.equal(got, want)
+    everything = torch.tensor([P + M + 500], dtype=torch.int32, device="cuda")
+    assert not torch.equal(lay.forward(x, None, y, attend=layers.Attend(c, start, table, everything)), want)
+    nvfp4.device_status()

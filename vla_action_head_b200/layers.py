@@ -56,8 +56,8 @@ def _rand(seed, shape, mean, std, device):
 class Attend:
     """What a layer with a key/value cache attends with.  cache: one sequence's NVFP4 cache of this
     layer; start: int32 [1], the cache row (and position) of the call's first token; table:
-    nvfp4.rope_table; kv_len: int32 [1], the keys after the call's rows are written (not needed to
-    fill the cache)."""
+    nvfp4.rope_table; kv_len: int32 [1], the keys after the call's rows are written (None: start and
+    the call's tokens; not needed to fill the cache)."""
     cache: nvfp4.KVCache
     start: torch.Tensor
     table: torch.Tensor
@@ -82,7 +82,8 @@ class _CacheAttention:
 
     def __call__(self, qkv, attend):
         self.store(qkv, attend)
-        nvfp4.attention(self.q, cache=attend.cache, kv_len=attend.kv_len, out=self.context, workspace=self.ws)
+        kv_len = attend.start + self.M if attend.kv_len is None else attend.kv_len
+        nvfp4.attention(self.q, cache=attend.cache, kv_len=kv_len, out=self.context, workspace=self.ws)
         return self.context.view(self.M, self.Hq * self.D)
 
 
