@@ -210,6 +210,11 @@ def test_a_workspace_of_another_device_is_refused(L):
         nvfp4.attention(q, k, k, workspace=nvfp4.Workspace("meta"))
 
 
+def test_a_layer_without_context_or_attend_says_so():
+    with pytest.raises(ValueError, match="attend"):
+        layers._CacheAttention(4, 8, 1, 256, "cpu")(torch.zeros(4, 2560, dtype=torch.bfloat16), None)
+
+
 def test_the_keys_of_a_layer_end_with_its_own_tokens(monkeypatch):
     """Without a kv_len: not with the cache's last row, which may never have been written."""
     seen = []

@@ -81,6 +81,8 @@ class _CacheAttention:
                            q_out=self.q)
 
     def __call__(self, qkv, attend):
+        if attend is None:
+            raise ValueError("a context, or attend, is needed")
         self.store(qkv, attend)
         kv_len = attend.start + self.M if attend.kv_len is None else attend.kv_len
         nvfp4.attention(self.q, cache=attend.cache, kv_len=kv_len, out=self.context, workspace=self.ws)
