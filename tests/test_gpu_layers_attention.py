@@ -184,3 +184,15 @@ def test_rows_behind_the_chunk_are_not_attended_to(prompt):
     everything = torch.tensor([P + M + 500], dtype=torch.int32, device="cuda")
     assert not torch.equal(lay.forward(x, None, y, attend=layers.Attend(c, start, table, everything)), want)
     nvfp4.device_status()
+
+
+def test_prompt_fills_the_cache_to_the_code(orc, prompt):
+    """Every code and scale, with the layer's own table."""
+    lay, att = prompt
+    qkv = lay.qkv_out.view(1, P, 10, 256).cpu()
+    k = ref.rotated(qkv[:, :, 8:9].float().numpy(), att.table.cpu().numpy(), np.arange(P)[None], 256, "half")
+    for x, codes, sf in ((k, att.cache.k_codes, att.cache.k_sf),
+                         (qkv[:, :, 9:].float().numpy(), att.cache.v_codes, att.cache.v_sf)):
+        c, s = ref.codes_of(orc, x, 1.0)
+        assert np.array_equal(codes[0, 0, :P].cpu().numpy(), c[0, :, 0])
+        assert np.array_equal(sf[0, 0, :P].cpu().numpy(), s[0, :, 0])
