@@ -196,3 +196,15 @@ def test_prompt_fills_the_cache_to_the_code(orc, prompt):
         c, s = ref.codes_of(orc, x, 1.0)
         assert np.array_equal(codes[0, 0, :P].cpu().numpy(), c[0, :, 0])
         assert np.array_equal(sf[0, 0, :P].cpu().numpy(), s[0, :, 0])
+
+
+def test_a_prompt_layer_turns_no_queries(orc, prompt):
+    """Filling the cache is all that `attend` asks of it: the same codes, and the place for queries stays."""
+    lay, att = prompt
+    before = [t.clone() for t in (att.cache.k_codes, att.cache.k_sf, att.cache.v_codes, att.cache.v_sf)]
+    c = nvfp4.empty_kv_cache(1, P + M, 1, 256)
+    lay.attention.q.fill_(7.0)
+    lay.forward(rand(P, 512), None, torch.empty(P, 512, dtype=torch.bfloat16, device="cuda"),
+                attend=layers.Attend(c, att.start, att.table))
+    assert (lay.attention.q == 7.0).all()
+    assert all(torch.equal(a, b) for a, b in zip(before, (c.k_codes, c.k_sf, c.v_codes, c.v_sf)))

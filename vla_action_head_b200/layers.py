@@ -73,12 +73,12 @@ class _CacheAttention:
         self.context = torch.empty((1, M, Hq, D), dtype=torch.bfloat16, device=device)
         self.ws = nvfp4.Workspace(device)
 
-    def store(self, qkv, attend):
-        """Turns keys, and queries into self.q; keys and values into the cache."""
+    def store(self, qkv, attend, queries=True):
+        """Turns keys, and queries into self.q (or leaves them out); keys and values into the cache."""
         qkv = qkv.view(1, self.M, self.Hq + 2 * self.Hkv, self.D)
         q, k, v = qkv.split([self.Hq, self.Hkv, self.Hkv], 2)
-        nvfp4.qk_norm_rope(q, k, table=attend.table, norm=False, v=v, cache=attend.cache, start=attend.start,
-                           q_out=self.q)
+        nvfp4.qk_norm_rope(q if queries else None, k, table=attend.table, norm=False, v=v, cache=attend.cache,
+                           start=attend.start, q_out=self.q if queries else None)
 
     def __call__(self, qkv, attend):
         if attend is None:
@@ -277,7 +277,7 @@ class PrefillLayer:
         nvfp4.quantize_norm(x, "rmsnorm", gamma=self.gamma1, eps=1e-6, out=self.a1)
         nvfp4.gemm(self.a1, self.qkv.w, "none", out=self.qkv_out, workspace=self.ws)
         if attend is not None:
-            self.attention.store(self.qkv_out, attend)
+            self.attention.store(self.qkv_out, attend, queries=False)
         nvfp4.quantize_norm(x, "rmsnorm", gamma=self.gamma2, eps=1e-6, out=self.a2)
         nvfp4.gemm(self.a2, self.gate_up.w, "geglu", out=self.u, workspace=self.ws)
         nvfp4.gemm(self.u, self.down.w, "residual", residual=x, out=y, workspace=self.ws)
