@@ -221,3 +221,65 @@ def test_nothing_is_read_behind_a_cached_head(orc, T, D):
         k = torch.full((16, 600, 16, 256), x, dtype=torch.bfloat16, device="cuda")
         nvfp4.attention(q, k, k)
         run_cache(orc, 2, T, 46, 8, 8, D)
+
+
+@pytest.mark.parametrize("T", [1, 20, 150])
+def test_keys_beyond_32_bits(orc, T):
+    """bf16 keys and values whose elements pass 2^32 along the keys, and along the batch together with the queries'
+    and the output's; a cache whose planes pass 2^32 bytes, under the tile kernel too."""
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB")
+    S, n, D, Hq = 17000000, 300, 256, 2
+    q = rand(2, T, Hq, D)
+    k, v = rand(2, n, 1, D, seed=1), rand(2, n, 1, D, seed=2)
+    want, bound = ref.attention_ref(q.double(), k.double(), v.double(), ref.default_scale(D))
+    mask = torch.zeros(1, S, dtype=torch.bool, device="cuda")
+    mask[0, S - n:] = True
+    long = [torch.zeros(1, S, 1, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    assert long[0].numel() > 1 << 32
+    for t, x in zip(long, (k, v)):
+        t[0, S - n:] = x[1].cuda()
+    out = nvfp4.attention(q[1:].cuda(), long[0], long[1], key_mask=mask)
+    ref.check(out, want[1:], bound[1:], "keys")
+    # two sequences, the second at the far end of the same memory
+    far = (S - n) * D
+    for t, x in zip(long, (k, v)):
+        t[0, :n] = x[0].cuda()
+    views = [t.as_strided((2, n, 1, D), (far, D, D, 1)) for t in long]
+    queries = torch.zeros(S * D, dtype=torch.bfloat16, device="cuda").as_strided((2, T, Hq, D), (far, Hq * D, D, 1))
+    queries.copy_(q)
+    ref.check(nvfp4.attention(queries, *views, out=queries), want, bound, "batch")
+    del long, views, queries
+    c = nvfp4.KVCache(*[torch.zeros((1, 1, 2 * S, D // m), dtype=torch.uint8, device="cuda") for m in (2, 16, 2, 16)])
+    assert c.k_codes.numel() > 1 << 32
+    small = rand_cache(1, 1, n, D)
+    for t, x in zip((c.k_codes, c.k_sf, c.v_codes, c.v_sf), (small.k_codes, small.k_sf, small.v_codes, small.v_sf)):
+        t[:, :, 2 * S - n:] = x[:, :, :n]
+    mask = torch.zeros(1, 2 * S, dtype=torch.bool, device="cuda")
+    mask[0, 2 * S - n:] = True
+    want, bound = ref.attention_ref(q[:1].double(), *cache_values(orc, small), ref.default_scale(D))
+    ref.check(nvfp4.attention(q[:1].cuda(), cache=c, key_mask=mask), want, bound, "cache")
+    nvfp4.device_status()
+
+
+def test_heads_beyond_32_bits():
+    """Norm + rotation in place, and a cache read, over sequences that lie 2^32 elements apart."""
+    T, D, far = 40, 128, (1 << 32) + 1024
+    if torch.cuda.mem_get_info()[0] < 30 << 30:
+        pytest.skip("needs 30 GB")
+    big = torch.zeros(far + T * 6 * D, dtype=torch.bfloat16, device="cuda")
+    x = big.as_strided((2, T, 6, D), (far, 6 * D, D, 1))
+    x.copy_(rand(2, T, 6, D))
+    small, table = x.contiguous(), nvfp4.rope_table(T, D)
+    a, b = nvfp4.qk_norm_rope(small[:, :, :4], small[:, :, 4:], table=table)
+    c = nvfp4.empty_kv_cache(2, T, 2, D)
+    nvfp4.kv_write(c, small[:, :, 4:], small[:, :, 4:])
+    d = nvfp4.empty_kv_cache(2, T, 2, D)
+    nvfp4.kv_write(d, x[:, :, 4:], x[:, :, 4:])
+    assert torch.equal(c.k_codes, d.k_codes) and torch.equal(c.v_sf, d.v_sf)
+    nvfp4.qk_norm_rope(x[:, :, :4], x[:, :, 4:], table=table, q_out=x[:, :, :4], k_out=x[:, :, 4:])
+    assert torch.equal(x[:, :, :4], a) and torch.equal(x[:, :, 4:], b)
+    k, v = nvfp4.kv_read(c)
+    nvfp4.kv_read(c, k_out=x[:, :, :2], v_out=x[:, :, 2:4])
+    assert torch.equal(x[:, :, :2], k) and torch.equal(x[:, :, 2:4], v)
+    nvfp4.device_status()
