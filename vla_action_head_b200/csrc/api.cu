@@ -1093,6 +1093,7 @@ nvfp4_status nvfp4_qk_norm_rope(const nvfp4_qk_args *x, nvfp4_stream_t stream) {
     a.start = x->start;
     a.count = x->count;
     a.cached = cached ? 1 : 0;
+    a.sms = sm_count_cached();
     if ((a.status = status_word()) == nullptr) return NVFP4_ERR_CUDA;
     cudaError_t e = launch_qk_norm_rope(a, stream);
     if (e == cudaSuccess) e = cudaGetLastError();

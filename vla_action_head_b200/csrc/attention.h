@@ -51,6 +51,7 @@ struct QkArgs {
     int cached;
     Cache cache;
     uint32_t *status;
+    int sms;                  // of the device
     FastDiv by_tokens, by_t;  // set by the launcher
     uint32_t items;          // groups of lanes: below 2^31
     double inv_d;

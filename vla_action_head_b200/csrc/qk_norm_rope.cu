@@ -414,7 +414,7 @@ cudaError_t launch_qk_norm_rope(const QkArgs &a, cudaStream_t s) {
     if (a.D % 32 == 0 && (a.inter || a.R == 0 || a.R == a.D)) {
         const int lanes = a.D / 16;  // 2 .. 16
         const double threads = static_cast<double>(a.B) * a.T * (a.Hq + (a.cached ? 2 : 1) * a.Hkv) * lanes;
-        const bool many = threads > 3.0 * 148 * 1024;
+        const bool many = threads > 3.0 * a.sms * 1024;
 #define NVFP4_LANES(N) \
     if (lanes <= N) return many ? launch_lph<N, kHeads, true>(a, s) : launch_lph<N, 1, true>(a, s);
         NVFP4_LANES(2) NVFP4_LANES(4) NVFP4_LANES(8) NVFP4_LANES(16)
