@@ -483,8 +483,8 @@ typedef struct {
 nvfp4_status nvfp4_qk_norm_rope(const nvfp4_qk_args *a, nvfp4_stream_t stream);
 
 /* Reads `length` rows of each sequence from row start[b] (device, [B]; NULL: 0) on back to
- * bf16: k_out, v_out [B, length, H, D], each element val(code) * dec(sf) (exact) * scale,
- * rounded once.  Rows outside [0, cache.length) are written as zeros, and reported as above.
+ * bf16: k_out, v_out [B, length, H, D], each element val(code) * dec(sf) (exact) * scale
+ * rounded to fp32, then to bf16 (one rounding where scale is a power of two).  Rows outside [0, cache.length) are written as zeros, and reported as above.
  * Either output's ptr may be NULL. */
 typedef struct {
     nvfp4_kv_cache cache;
@@ -500,7 +500,8 @@ typedef struct {
     int Hq, Hkv;    /* Hq % Hkv == 0: query head h reads key head h / (Hq / Hkv) */
     int D;          /* head size: D % 8 == 0, 8 <= D <= 256 (a cache: D % 16 == 0) */
     float scale;    /* > 0, finite */
-    nvfp4_heads q, k, v, out;    /* k, v [B, S, Hkv, D] bf16: without a cache only */
+    nvfp4_heads q, k, v, out;    /* k, v [B, S, Hkv, D] bf16: without a cache only; keys (stride_t) are
+                                    not broadcast */
     const int32_t *kv_len;       /* [B] keys of each sequence, clamped to [0, S]; NULL: S */
     const uint8_t *key_mask;     /* [B, S], 0: the key is left out; NULL: none is */
     int64_t mask_stride;         /* elements between the mask's sequences */
@@ -511,8 +512,10 @@ typedef struct {
 /* out[b, t, h] = sum_j p_j v_j,  p = softmax_j(scale * q[b, t, h] . k_j) over the keys
  * j < kv_len[b] with key_mask[b, j] != 0; zero where there is no such key.  What the keys and
  * values of left-out places hold (infinities and NaN too) has no influence.  Scores,
- * statistics and sums are fp32; the softmax weights are rounded to bf16 (bf16 keys and
- * values) or fp16 (cache) for their product with the values; out is rounded once to bf16.
+ * statistics and sums are fp32 (scores that are infinite times scale * log2(e) may give NaN);
+ * the softmax weights are rounded to bf16 (bf16 keys and values) or fp16 (cache; small ones are
+ * off by up to 2^-32 of the largest) for their product with the values; out is rounded once to
+ * bf16.
  * B, T, S = 0: nothing is read (S = 0: zeros are written).  Results do not depend on timing.
  * workspace: nvfp4_attention_workspace_bytes, used by one call at a time, any contents.  Its first
  * 16 KiB are left alone, so a workspace of nvfp4_gemm may serve both, one after another. */

@@ -12,15 +12,17 @@
 // accumulator into the next operand by one 8 x 8 transposition in registers (movmatrix).
 //
 // Cache: codes become fp16 (exact: 2-bit significand times 4-bit scale; the weights are then fp16
-// too, closer than bf16).  Query rows are scaled by a power of two into fp16's range, which changes no bit of them.
+// too, closer than bf16).  Query rows are scaled by a power of two into fp16's range, which keeps every bit of an
+// element down to 2^-31 of the row's largest; smaller ones are off by 2^-39 of it at most.
 //
 // Every warp takes steps of 16 keys of its own: its lane 0 asks the copy engine for the next step's
 // rows (a tensor copy whose 128-byte swizzle makes the reads above free of bank conflicts; plain
 // bulk copies where a cache row is no multiple of 16 bytes), and the warp waits on its own barrier.
 // No barrier of the CTA in the loop, a few instructions a step for the loads.  (8 sequences of 32701
 // cached keys, 256-wide heads: 71 us with loads into registers, 46 with cp.async by every thread, 34 so,
-// 31 with the CTAs dealt out by the lengths, 28.7 with the pieces joined eight at a time.  Bound by the instructions
-// that turn codes into numbers, and by about 4 us of start and join.)
+// 31 with the CTAs dealt out by the lengths, 29.1 with the pieces joined eight at a time, 29.5 with weights that
+// reach down to 2^-32.  Bound by the instructions that turn codes into numbers, and by about 4 us of start and join.
+// The same over bf16 keys: 45 us, 76 % of the rate that a copy reaches.)
 //
 // The warps of a CTA are joined through shared memory.  A CTA takes a whole key head, or (long keys,
 // few heads) a piece of one, dealt out by the sequences' lengths (attention_share.cuh); the pieces are

@@ -16,7 +16,9 @@
 // Bound by instructions before memory (66-69 % of the issue slots).  16 x 968 tokens of 24 heads of 128 (190 MB):
 // 93 us with 64-bit index divisions and fp64 division and root; 47 us with indexes by multiplication, the root by
 // Newton steps and both halves in a lane; 39 us with packed fp32 pairs and four heads a group, which is 74 % of
-// the rate that a copy reaches.  The cache write of 16 x 968 tokens of 8 + 1 + 1 heads of 256: 102, 56, 46 us.
+// the rate that a copy reaches.  The cache write of 16 x 968 tokens of 8 + 1 + 1 heads of 256 and its read back:
+// 102, 56, 46 us; the write alone 41.  one_run, 64 of 128 elements turned by halves, 24 heads: 91 us, with a head's
+// 16 bytes a lane on their way and gamma and the angles fetched for every head.
 #include <cuda_runtime.h>
 
 #include <atomic>

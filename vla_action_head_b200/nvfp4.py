@@ -317,7 +317,8 @@ class Workspace:
     (re)allocated, reused across calls.
 
     A buffer that became too small is kept as long as the workspace: a captured graph holds its
-    address.  Each is at least twice the last, so all of them are below twice the largest."""
+    address.  Each is at least twice the last, so all of them are below twice the largest.  One that
+    is allocated while a graph is captured is zeroed by the replay: call once before capturing."""
 
     def __init__(self, device="cuda"):
         self.device = device
@@ -381,7 +382,8 @@ def probe():
 
 
 def device_status():
-    """Raises NVFP4Error(TIMEOUT) if a kernel's bounded wait expired since the last check."""
+    """Raises NVFP4Error if, since the last check, a kernel's bounded wait expired (TIMEOUT) or a position
+    or cache row did not exist (INVALID_ARG)."""
     _check("nvfp4_get_device_status", lib().nvfp4_get_device_status(_stream()))
 
 
