@@ -198,10 +198,10 @@ def test_a_workspace_keeps_the_buffers_it_outgrew():
 
 @pytest.mark.parametrize("kw", [dict(T=1, S=40000, B=1), dict(T=50, S=9000, B=1), dict(T=200, S=3000, B=2, D=128)], ids=str)
 def test_parts_lie_behind_the_counters_of_gemms(L, kw):
-    """A workspace is 16 KiB of GEMM counters, then whole parts: D sums, a reference and a sum of weights a row."""
+    """A workspace is 16 KiB of GEMM counters, then whole parts: D sums and four numbers more a row."""
     D = kw.get("D", 256)
     need = L.nvfp4_attention_workspace_bytes(C.byref(at(**kw)))
-    assert need > 16384 and (need - 16384) % (4 * (D + 2)) == 0
+    assert need > 16384 and (need - 16384) % (4 * (D + 4)) == 0
 
 
 def test_a_workspace_of_another_device_is_refused(L):

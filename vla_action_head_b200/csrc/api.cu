@@ -560,7 +560,7 @@ size_t attention_part_rows(const AttnArgs &a) {
 // Behind the GEMMs' counters, which a workspace that serves both must keep zero.
 size_t attention_workspace(const AttnArgs &a) {
     const size_t rows = attention_part_rows(a);
-    return rows == 0 ? 0 : kTicketRegion + rows * (a.D + 2) * sizeof(float);
+    return rows == 0 ? 0 : kTicketRegion + rows * (a.D + 4) * sizeof(float);
 }
 
 // The arguments of nvfp4_attention, without device access; `empty`: there is nothing to write.
@@ -1152,7 +1152,7 @@ nvfp4_status nvfp4_attention(const nvfp4_attention_args *x, void *workspace, siz
         if (workspace == nullptr || ws_bytes < need) return NVFP4_ERR_WORKSPACE;
         if (!aligned16(workspace)) return NVFP4_ERR_MISALIGNED;
         a.part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kTicketRegion);
-        a.part_ml = reinterpret_cast<float2 *>(a.part_o + attention_part_rows(a) * a.D);
+        a.part_ml = reinterpret_cast<float4 *>(a.part_o + attention_part_rows(a) * a.D);
     }
     st = check_device();
     if (st != NVFP4_OK) return st;

@@ -84,11 +84,13 @@ struct AttnArgs {
     int cluster;     // tile kernel: 1: the parts are a cluster, which joins them; 0: from part_o and part_ml
     int share;       // row kernel: > 0: CTAs dealt out by the lengths, joined; 0: a CTA a key head
     int warps;       // row kernel: of a CTA
-    // unnormalized sums; references in units of log2 and sums of weights.
+    // unnormalized sums; per row its reference score, its sum of weights and its score factor (one value in
+    // all parts).  (Not the product of the first and the last: its rounding would weigh the parts of large scores
+    // differently than a part weighs its keys.)
     // tile kernel: [key heads, row tiles, splits, D / 4, part_rows(), 4] and [.., splits, part_rows()], so that
     // rows in a warp's lanes are adjacent; row kernel: [CTAs, rows of a key head] (x D)
     float *part_o;
-    float2 *part_ml;
+    float4 *part_ml;
     uint32_t *status;
     __host__ __device__ int row_tiles() const { return (T * G + 127) >> 7; }
     __host__ __device__ int part_rows() const { return T * G >= 128 ? 128 : (T * G + 31) & ~31; }

@@ -18,7 +18,7 @@ namespace {
 constexpr int kThreads = 128;  // also the rows of a tile
 
 // With M the largest reference of the parts that have a sum,
-// out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s (references in units of log2), in the order of s.
+// out = sum_s 2^(c (m_s - M)) O_s / sum_s 2^(c (m_s - M)) l_s, in the order of s.
 
 // The tile kernel's parts: a thread a row and 8 columns; adjacent rows lie side by side.
 __global__ void __launch_bounds__(kThreads) attention_join_tiles_kernel(const AttnArgs p) {
@@ -29,14 +29,14 @@ __global__ void __launch_bounds__(kThreads) attention_join_tiles_kernel(const At
     const int tile = id % tiles, bh = id / tiles, hk = bh % p.Hkv, b = bh / p.Hkv;
     const int r = static_cast<int>(threadIdx.x), row = tile * 128 + r;
     if (row >= rows) return;
-    const float2 *ml = p.part_ml + static_cast<size_t>(id) * p.splits * pr + r;
+    const float4 *ml = p.part_ml + static_cast<size_t>(id) * p.splits * pr + r;
     const size_t step = static_cast<size_t>(p.D >> 2) * pr;  // from a part to the next, in float4
     const float4 *po = reinterpret_cast<const float4 *>(p.part_o) + id * p.splits * step + 2 * static_cast<size_t>(cg) * pr + r;
     // eight parts at a time, all their loads in flight together
     constexpr int kParts = 8;
-    float M = -INFINITY, l = 0.0f, o[8] = {};
+    float M = -INFINITY, l = 0.0f, c = 0.0f, o[8] = {};
     for (int s0 = 0; s0 < p.splits; s0 += kParts) {
-        float2 x[kParts];
+        float4 x[kParts];
         float4 u[kParts], v[kParts];
 #pragma unroll
         for (int i = 0; i < kParts; ++i) {
@@ -49,15 +49,15 @@ __global__ void __launch_bounds__(kThreads) attention_join_tiles_kernel(const At
         const float before = M;
 #pragma unroll
         for (int i = 0; i < kParts; ++i)
-            if (x[i].y != 0.0f) M = fmaxf(M, x[i].x);
-        const float g = before == -INFINITY ? 0.0f : exp2f(before - M);
+            if (x[i].y != 0.0f) M = fmaxf(M, x[i].x), c = x[i].z;
+        const float g = before == -INFINITY ? 0.0f : exp2f((before - M) * c);
         l *= g;
 #pragma unroll
         for (int k = 0; k < 8; ++k) o[k] *= g;
 #pragma unroll
         for (int i = 0; i < kParts; ++i)
             if (x[i].y != 0.0f) {  // a part without keys may hold anything
-                const float f = exp2f(x[i].x - M);
+                const float f = exp2f((x[i].x - M) * c);
                 l = fmaf(f, x[i].y, l);
                 const float y[8] = {u[i].x, u[i].y, u[i].z, u[i].w, v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
@@ -88,10 +88,10 @@ __global__ void __launch_bounds__(kThreads) attention_join_kernel(const AttnArgs
     int len;
     const int steps = key_steps(p, b, &len), piece = key_piece(p), parts = (steps + piece - 1) / piece;
     const size_t first = static_cast<size_t>(first_piece(p, b, hk, piece, steps)) * rows + r, step = rows;
-    const float2 *ml = p.part_ml + first;
+    const float4 *ml = p.part_ml + first;
     float M = -INFINITY;
     for (int s = lane; s < parts; s += 32) {
-        const float2 x = __ldcg(ml + s * step);
+        const float4 x = __ldcg(ml + s * step);
         if (x.y != 0.0f) M = fmaxf(M, x.x);
     }
 #pragma unroll
@@ -102,8 +102,8 @@ __global__ void __launch_bounds__(kThreads) attention_join_kernel(const AttnArgs
     for (int s0 = 0; s0 < parts; s0 += 32) {
         float f = 0.0f;
         if (s0 + lane < parts) {
-            const float2 x = __ldcg(ml + (s0 + lane) * step);
-            if (x.y != 0.0f) f = exp2f(x.x - M);
+            const float4 x = __ldcg(ml + (s0 + lane) * step);
+            if (x.y != 0.0f) f = exp2f((x.x - M) * x.z);
             l = fmaf(f, x.y, l);
         }
         const int n = min(32, parts - s0);

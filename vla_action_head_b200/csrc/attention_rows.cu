@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(Cfg<DP, FULL, CACHED>::kThreads, 1)
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
         if (g == 0) {
-            sm_m[warp][2 * t + i] = m[i] * cr[i];  // in units of log2
+            sm_m[warp][2 * t + i] = m[i];
             sm_l[warp][2 * t + i] = l[i];
         }
 #pragma unroll
@@ -469,17 +469,18 @@ __global__ void __launch_bounds__(Cfg<DP, FULL, CACHED>::kThreads, 1)
     __syncthreads();
     // each warp's factor against the row's largest reference, and the row's sum
     for (int r = warp; r < rows; r += kWarps) {
+        const float c = score_factor(p.scale_log2, sm_q[r]);
         const float lw = lane < kWarps ? sm_l[lane][r] : 0.0f, mw = lane < kWarps && lw != 0.0f ? sm_m[lane][r] : -INFINITY;
         float M = mw;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-        const float f = lw != 0.0f ? ex2(sm_m[lane][r] - M) : 0.0f;
+        const float f = lw != 0.0f ? ex2((sm_m[lane][r] - M) * c) : 0.0f;
         float sum = f * lw;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
         if (lane < kWarps) sm_l[lane][r] = f;
         if (lane == 0) sm_q[r] = sum;
-        if (lane == 0 && p.share > 0) p.part_ml[static_cast<size_t>(blockIdx.x) * rows + r] = make_float2(M, sum);
+        if (lane == 0 && p.share > 0) p.part_ml[static_cast<size_t>(blockIdx.x) * rows + r] = make_float4(M, sum, c, 0.0f);
     }
     __syncthreads();
     // a thread: every kThreads-th pair of elements of the rows

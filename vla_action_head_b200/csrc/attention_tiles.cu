@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(Cfg<DP, CACHED>::kThreads, 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 1);
     float *row_factor = reinterpret_cast<float *>(smem + C::kOffRow);
     float *maxima = reinterpret_cast<float *>(smem + C::kOffMax);
-    float2 *part_ml = reinterpret_cast<float2 *>(smem);  // in a cluster, where Q was: reference, sum of weights
+    float4 *part_ml = reinterpret_cast<float4 *>(smem);  // in a cluster, where Q was: as in p.part_ml
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     // the CTA's place: split fastest, then row tile, key head, sequence
@@ -607,8 +607,8 @@ __global__ void __launch_bounds__(Cfg<DP, CACHED>::kThreads, 1)
                 const int pr = p.part_rows();
                 const size_t part = ((static_cast<size_t>(b) * p.Hkv + hk) * p.row_tiles() + (first >> 7)) * p.splits + split;
                 float4 *to = reinterpret_cast<float4 *>(p.part_o) + part * (p.D >> 2) * pr + row;
-                if (half == 0 && p.cluster) part_ml[first - row0 + row] = make_float2(m * c, l);
-                else if (half == 0 && lane < live) p.part_ml[part * pr + row] = make_float2(m * c, l);
+                if (half == 0 && p.cluster) part_ml[first - row0 + row] = make_float4(m, l, c, 0.0f);
+                else if (half == 0 && lane < live) p.part_ml[part * pr + row] = make_float4(m, l, c, 0.0f);
                 for (int e = 32 * half; e < p.D && n > 0; e += 64) {
                     uint32_t o[32];
                     tmem_ld_32x32b_x32(o_base + e, o);
@@ -680,7 +680,9 @@ __global__ void __launch_bounds__(Cfg<DP, CACHED>::kThreads, 1)
             const uint32_t at = sbase + C::kOffRing + (r >> 5) * 32 * C::kOutPitch + (r & 31) * (p.D * 4 + 16) + e * 4;
             float2 part[kAttentionCluster];
             float4 y0[kAttentionCluster], y1[kAttentionCluster];
+            // (the first part has keys if any has, and so the row's factor)
             float M = -INFINITY;
+            const float c = CACHED ? ld_dsmem_f2(mapa_shared(ml + 8, 0)).x : p.scale_log2;
 #pragma unroll
             for (int q = 0; q < kAttentionCluster; ++q) {
                 part[q] = make_float2(-INFINITY, 0.0f);
@@ -697,7 +699,7 @@ __global__ void __launch_bounds__(Cfg<DP, CACHED>::kThreads, 1)
 #pragma unroll
             for (int q = 0; q < kAttentionCluster; ++q)
                 if (part[q].y != 0.0f) {  // a part without keys holds nothing
-                    const float f = ex2(part[q].x - M);
+                    const float f = ex2((part[q].x - M) * c);
                     sum = fmaf(f, part[q].y, sum);
                     const float y[8] = {y0[q].x, y0[q].y, y0[q].z, y0[q].w, y1[q].x, y1[q].y, y1[q].z, y1[q].w};
 #pragma unroll
