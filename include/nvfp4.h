@@ -512,7 +512,7 @@ typedef struct {
 /* out[b, t, h] = sum_j p_j v_j,  p = softmax_j(scale * q[b, t, h] . k_j) over the keys
  * j < kv_len[b] with key_mask[b, j] != 0; zero where there is no such key.  What the keys and
  * values of left-out places hold (infinities and NaN too) has no influence.  Scores,
- * statistics and sums are fp32 (products q . k beyond it give NaN, scaled ones may be beyond it);
+ * statistics and sums are fp32 (a q . k beyond it may give NaN; scaled, it may be beyond it);
  * the softmax weights are rounded to bf16 (bf16 keys and values) or fp16 (cache; small ones are
  * off by up to 2^-32 of the largest) for their product with the values; out is rounded once to
  * bf16.
